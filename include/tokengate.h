@@ -60,7 +60,8 @@ typedef enum {
   TG_OP_GATED_ATTN = 3,
   TG_OP_PREFILL = 4,
   TG_OP_DECODE = 5,  /* shape: d_model, heads, head_dim, d_ffn, k = kept prompt tokens, dtype */
-  TG_OP_GATED_ATTN_BWD = 6  /* shape: k = rows, heads, head_dim */
+  TG_OP_GATED_ATTN_BWD = 6, /* shape: k = rows, heads, head_dim */
+  TG_OP_PAGED_ATTN = 7      /* shape: n = batch, k = rows, heads, head_dim, dtype */
 } tg_op;
 
 /* Sizes used to size a workspace; fields an op does not use are ignored. */
@@ -521,6 +522,129 @@ tg_status tg_decode_step(const tg_model* model, const void* x, int64_t pos, int3
                          const int32_t* kept_idx, int64_t k_kept, void* out, void* ws,
                          size_t ws_bytes, tg_stream stream);
 
+/* ---- serving from a paged cache -------------------------------------------
+ *
+ * tg_prefill and tg_decode_step keep one request's KV in one buffer per layer.
+ * A process that serves many requests keeps the cache of a layer in a pool of
+ * pages instead: row j of request b sits in page table[b][j / page_size], row
+ * j % page_size. Layers above the gate hold the kept tokens' rows and, beside
+ * each key, its gate bias logsigmoid(s_j) (0 for generated rows: generated
+ * tokens are never pruned, and the bias fixed at prefill acts as an additive
+ * mask, [TC] "TokenGate 提前筛选 Token", "TokenGate 的工程验证仍有限"); the layers
+ * at and below it hold every row. The pages are not described further; the
+ * page layout is this library's choice.
+ *
+ * A call works on the new rows of a batch of requests, one layer at a time:
+ *   cu_q    [batch + 1] int32, ascending from 0: request b owns rows
+ *           cu_q[b] .. cu_q[b+1] - 1 of q, k and v (it may own none). Rows
+ *           from cu_q[batch] on are neither read nor written.
+ *   kv_len  [batch] int32: the cached rows of the request, its new rows
+ *           included. New row i is cache row kv_len[b] - n_b + i.
+ * cu_q, kv_len, the table and the positions are device data, so a captured
+ * call can be replayed as the cache grows. They are checked on the device: a
+ * row or page out of range is skipped (a skipped key counts as a key of
+ * zeros) and sets bit 2 of the device error word.
+ */
+typedef struct {
+  void* k;               /* pages of [page_size, n_heads_kv, head_dim] dtype, keys rotated   */
+  void* v;               /* the same for the values                                          */
+  float* bias;           /* pages of [page_size] fp32: gate biases, or NULL (no bias)        */
+  const int32_t* table;  /* [batch, table_stride]; entries behind a request's rows are free  */
+  int64_t n_pages;
+  int64_t k_page_stride; /* elements between pages (a pool may interleave layers):           */
+  int64_t v_page_stride; /*   >= page_size n_heads_kv head_dim, in 16-byte multiples         */
+  int64_t bias_page_stride; /* >= page_size                                                  */
+  int32_t table_stride;
+  int32_t page_size;     /* 16, 32, 64, 128 or 256                                           */
+  int32_t n_heads_kv;
+  int32_t head_dim;      /* 64 or 128                                                        */
+  tg_dtype dtype;
+} tg_paged_kv;
+
+/*
+ * tg_paged_append -- what lies between a layer's QKV projection and its
+ * attention: the optional per-head RMSNorm of q and k, their rotation (RoPE
+ * as in tg_gated_attn_prefill), and k, v and the gate biases into the pages.
+ *   q [rows, hq, dh], k, v [rows, hkv, dh] dtype with q_stride / k_stride /
+ *     v_stride elements between rows (the slices of a fused projection's
+ *     output, for instance; 16-byte aligned and in 16-byte multiples).
+ *     q may be NULL (hq 0): only the cache is written.
+ *   pos [rows] int32: the original positions, or NULL: row index kv_len[b] -
+ *     n_b + i of the request.
+ *   s [rows] fp32: gate scores of kept rows (bias logsigmoid(s)), or NULL
+ *     (bias 0). Unused when the cache holds no bias.
+ *   q_norm, k_norm [dh] fp32 or NULL (each on its own), eps: y = x /
+ *     sqrt(mean(x^2) + eps) * w per head.
+ *   rope_base > 0, or 0: no rotation (keys that are rotated already, such as
+ *     those that tg_prefill writes).
+ *   q_out [rows, hq, dh] dtype: the queries for tg_paged_attn; may be q
+ *     itself where its rows are q_stride = hq dh apart.
+ * Two requests must not append to the same page row. bf16 or fp32.
+ */
+tg_status tg_paged_append(const tg_paged_kv* cache, const void* q, int64_t q_stride, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, int64_t rows,
+                          const int32_t* cu_q, const int32_t* kv_len, int32_t batch, int32_t hq,
+                          const int32_t* pos, const float* s, const float* q_norm,
+                          const float* k_norm, float eps, float rope_base, void* q_out,
+                          tg_stream stream);
+
+/*
+ * tg_paged_attn -- token-gated causal GQA attention of chunks of new tokens
+ * over the paged cache: one token of each request (decoding), drafted tokens,
+ * or a chunk of a prompt; lengths may differ freely within a batch.
+ *   l_ij = (q_i . k_j) / (sqrt(dh) * tau_h) + gain_h * bias_j
+ *     over cache rows j < kv_len[b] - n_b + i + 1 for new row i of request b,
+ *   o_i = sum_j softmax_j(l_ij) v_j
+ *   q [rows, hq, dh] dtype, rotated, q_stride elements between rows (16-byte
+ *     aligned, in 16-byte multiples); head h reads KV head h / (hq / hkv)
+ *   gain [hq] fp32 or NULL (0: no bias); tau [hq] fp32 > 0 or NULL (1)
+ *   max_kv: no kv_len of the call is above it (a longer one is cut there and
+ *     reported); at most table_stride page_size. It only has to hold, but a
+ *     close one lets the call size its launch closely.
+ *   out [rows, hq, dh] dtype; lse [hq, rows] fp32 or NULL: log sum_j exp(l_ij)
+ * A logit of -inf, or below -1e30 (log2 units), such as that of a bias of
+ * -inf, removes the key; a row that has no key left (or kv_len[b] < n_b)
+ * gets zeros and lse -inf. Values of keys that a row does not see never reach
+ * it, whatever they hold. The chunk's own rows must be in the cache
+ * (tg_paged_append). Workspace: tg_workspace_size(TG_OP_PAGED_ATTN) with
+ * n = batch, k = rows, the heads, head_dim and dtype; it carries nothing from
+ * call to call. bf16 (products of bf16 values on the tensor cores, sums and
+ * softmax in fp32) or fp32 (CUDA cores).
+ */
+tg_status tg_paged_attn(const tg_paged_kv* cache, const void* q, int64_t q_stride, int64_t rows,
+                        const int32_t* cu_q, const int32_t* kv_len, int32_t batch, int32_t hq,
+                        int64_t max_kv, const float* gain, const float* tau, void* out, float* lse,
+                        void* ws, size_t ws_bytes, tg_stream stream);
+
+/* ---- 8-bit projections ----------------------------------------------------
+ *
+ * tg_quantize_rows -- rows of 8-bit integers with one scale each, for
+ * tg_linear_quantized: activations (one scale per token) or, once per model,
+ * a weight matrix [out, in] (one scale per output channel).
+ *   scale_i = max_j |x_ij| / 127,  xq_ij = rint(127 x_ij / max_j |x_ij|)
+ * with the quotient rounded once, ties to even. A row of zeros has scale 0; a
+ * row that holds an infinity or a NaN has zeros and scale NaN, so that its
+ * products are NaN.
+ *   x [rows, cols] bf16 or fp32, x_stride elements between rows (16-byte
+ *     aligned, in 16-byte multiples); cols % 16 == 0
+ *   xq [rows, cols] int8 (16-byte aligned), scale [rows] fp32
+ */
+tg_status tg_quantize_rows(const void* x, int64_t x_stride, int64_t rows, int32_t cols,
+                           tg_dtype dtype, int8_t* xq, float* scale, tg_stream stream);
+
+/*
+ * tg_linear_quantized -- tg_linear on 8-bit integers:
+ *   y_ij = (sum_k xq_ik wq_jk) xs_i ws_j (+ residual_ij)
+ * the sum exact in 32-bit integers, the rest in fp32, rounded once to dtype.
+ *   xq [m, k], wq [n, k] int8 (16-byte aligned; any values, -128 included);
+ *   xs [m], ws [n] fp32; residual [m, n] dtype or NULL (may equal y);
+ *   y [m, n] dtype, bf16 or fp32.
+ * n % 32 == 0, k % 16 == 0, k <= 131056 (else TG_ERR_UNSUPPORTED).
+ */
+tg_status tg_linear_quantized(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws,
+                              const void* residual, int64_t m, int32_t n, int32_t k, tg_dtype dtype,
+                              void* y, tg_stream stream);
+
 /* ---- the Gated DeltaNet mixer on its own (tg_gdn_layer is above) -------- */
 
 /* Workspace bytes of tg_gated_deltanet for T tokens (0 for a bad layer). */
@@ -587,7 +711,11 @@ typedef enum {
   TG_K_GDN_RECUR = 22,       /* Gated DeltaNet: the state across the chunks          */
   TG_K_GDN_OUT = 23,         /* Gated DeltaNet: gated output RMSNorm                 */
   TG_K_FOLD_NORM = 24,       /* tg_fold_norm_weight                                  */
-  TG_K_COUNT = 25
+  TG_K_PAGED_APPEND = 25,    /* tg_paged_append                                      */
+  TG_K_PAGED_ATTN = 26,      /* tg_paged_attn                                        */
+  TG_K_QUANTIZE = 27,        /* tg_quantize_rows                                     */
+  TG_K_GEMM_INT = 28,        /* tg_linear_quantized                                  */
+  TG_K_COUNT = 29
 } tg_kernel;
 
 typedef struct {

@@ -32,7 +32,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 TG_OK, TG_ERR_INVALID_ARG, TG_ERR_UNSUPPORTED, TG_ERR_BUDGET, TG_ERR_WORKSPACE, TG_ERR_CUDA = range(6)
 TG_F32, TG_BF16 = 0, 1
 (TG_OP_SCORE, TG_OP_TOPK_SELECT, TG_OP_COMPACT, TG_OP_GATED_ATTN, TG_OP_PREFILL, TG_OP_DECODE,
- TG_OP_GATED_ATTN_BWD) = range(7)
+ TG_OP_GATED_ATTN_BWD, TG_OP_PAGED_ATTN) = range(8)
 
 _c_i32, _c_i64, _c_f32, _c_p, _c_sz = (ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
                                        ctypes.c_void_p, ctypes.c_size_t)
@@ -73,6 +73,13 @@ class TgGdnLayer(ctypes.Structure):
     _fields_ = [("n_heads_k", _c_i32), ("n_heads_v", _c_i32), ("head_dim_k", _c_i32),
                 ("head_dim_v", _c_i32), ("conv_width", _c_i32), ("conv_w", _c_p),
                 ("A_log", _c_p), ("dt_bias", _c_p), ("norm_w", _c_p), ("norm_eps", _c_f32)]
+
+
+class TgPagedKv(ctypes.Structure):
+    _fields_ = [("k", _c_p), ("v", _c_p), ("bias", _c_p), ("table", _c_p), ("n_pages", _c_i64),
+                ("k_page_stride", _c_i64), ("v_page_stride", _c_i64),
+                ("bias_page_stride", _c_i64), ("table_stride", _c_i32), ("page_size", _c_i32),
+                ("n_heads_kv", _c_i32), ("head_dim", _c_i32), ("dtype", ctypes.c_int)]
 
 
 class TgTraceRecord(ctypes.Structure):
@@ -124,6 +131,14 @@ _decode = _sig("tg_decode_step", _ci, ctypes.POINTER(TgModel), _c_p, _c_i64, _c_
 _gdn_ws = _sig("tg_gated_deltanet_workspace_size", _c_sz, ctypes.POINTER(TgGdnLayer), _c_i64)
 _gdn = _sig("tg_gated_deltanet", _ci, ctypes.POINTER(TgGdnLayer), _c_p, _c_p, _c_p, _c_p, _c_i64,
             _ci, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p)
+_paged_append = _sig("tg_paged_append", _ci, ctypes.POINTER(TgPagedKv), _c_p, _c_i64, _c_p, _c_i64,
+                     _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i32, _c_i32, _c_p, _c_p, _c_p, _c_p,
+                     _c_f32, _c_f32, _c_p, _c_p)
+_paged_attn = _sig("tg_paged_attn", _ci, ctypes.POINTER(TgPagedKv), _c_p, _c_i64, _c_i64, _c_p,
+                   _c_p, _c_i32, _c_i32, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p)
+_quantize = _sig("tg_quantize_rows", _ci, _c_p, _c_i64, _c_i64, _c_i32, _ci, _c_p, _c_p, _c_p)
+_linear_q = _sig("tg_linear_quantized", _ci, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_i32, _c_i32,
+                 _ci, _c_p, _c_p)
 _status_string = _sig("tg_status_string", ctypes.c_char_p, _ci)
 _last_cuda_error = _sig("tg_last_cuda_error", _ci)
 _device_error = _sig("tg_device_error", _ci, ctypes.POINTER(ctypes.c_uint32), _ci)
@@ -650,6 +665,212 @@ def tg_prefill_batch(model: Model, x, protect, lens: Sequence[int], ks: Sequence
     return out, kept_idx, scores
 
 
+# ----------------------------------------------------------------- paged cache
+
+
+class _on:
+    """Makes `device` the current one for a call (nothing to do when it is)."""
+
+    __slots__ = ("dev", "prev")
+
+    def __init__(self, device):
+        _need(device.type == "cuda", "tensors must be on a CUDA device")
+        self.dev = device.index
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        self.prev = None if cur == self.dev else cur
+        if self.prev is not None:
+            torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            torch.cuda.set_device(self.prev)
+
+
+def _need(cond: bool, what: str) -> None:
+    if not cond:
+        raise ValueError(what)
+
+
+def _vec(t, n: int, dtype, device, name: str):
+    """Pointer of an optional contiguous 1-D tensor of n elements."""
+    if t is None:
+        return None
+    _need(t.dtype == dtype and t.device == device and t.numel() == n and t.is_contiguous(),
+          f"{name} must be a contiguous {dtype} tensor of {n} elements on {device}")
+    return t.data_ptr()
+
+
+def _rows3(t, rows: int, heads: int, dh: int, dtype, device, name: str) -> int:
+    """Row stride of a [rows, heads, dh] tensor whose rows are contiguous."""
+    _need(t.dtype == dtype and t.device == device and t.shape == (rows, heads, dh),
+          f"{name} must be {dtype} [{rows}, {heads}, {dh}] on {device}")
+    if rows == 0:
+        return heads * dh
+    s0, s1, s2 = t.stride()
+    _need(s2 == 1 and (heads == 1 or s1 == dh), f"{name}: each row must be contiguous")
+    return s0 if rows > 1 else max(s0, heads * dh)
+
+
+class PagedKV:
+    """One layer's paged key/value cache: k, v [n_pages, page_size, hkv, dh]
+    (bf16 or fp32; a page must be contiguous, pages may be apart, so a layer
+    of a pool [n_pages, n_layers, ...] will do), table [batch, max_pages]
+    int32 (page of each block of page_size rows of a request) and optionally
+    bias [n_pages, page_size] fp32 (gate biases logsigmoid(s), 0 = none)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
+                 bias: Optional[torch.Tensor] = None):
+        _need(k.dim() == 4 and v.shape == k.shape and v.dtype == k.dtype and k.device == v.device,
+              "k and v must be [n_pages, page_size, hkv, dh] of one dtype and device")
+        n_pages, ps, hkv, dh = k.shape
+        for name, t in (("k", k), ("v", v)):
+            _need(n_pages == 0 or t[0].is_contiguous(), f"{name}: each page must be contiguous")
+        _need(table.dim() == 2 and table.dtype == torch.int32 and table.is_contiguous()
+              and table.device == k.device, "table must be a contiguous int32 [batch, max_pages]")
+        if bias is not None:
+            _need(bias.dtype == torch.float32 and bias.shape == (n_pages, ps)
+                  and bias.device == k.device and (ps == 1 or bias.stride(1) == 1),
+                  "bias must be fp32 [n_pages, page_size]")
+        self.k, self.v, self.table, self.bias = k, v, table, bias
+        self.page_size, self.n_heads_kv, self.head_dim = ps, hkv, dh
+        self.dtype, self.device = k.dtype, k.device
+        page = ps * hkv * dh
+
+        def apart(t, least):
+            return t.stride(0) if n_pages > 1 else max(t.stride(0), least)
+
+        self.c = TgPagedKv(k.data_ptr(), v.data_ptr(), None if bias is None else bias.data_ptr(),
+                           table.data_ptr(), n_pages, apart(k, page), apart(v, page),
+                           0 if bias is None else apart(bias, ps), table.shape[1], ps, hkv, dh,
+                           _dt(k))
+        self._ref = ctypes.byref(self.c)
+
+    @property
+    def batch(self) -> int:
+        return self.table.shape[0]
+
+    @property
+    def capacity(self) -> int:
+        """Rows that the table has room for, per request."""
+        return self.table.shape[1] * self.page_size
+
+
+def tg_paged_append(cache: PagedKV, k, v, cu_q, kv_len, q=None, pos=None, s=None, q_norm=None,
+                    k_norm=None, eps: float = 1e-6, rope_base: float = 1e6, q_out=None,
+                    stream=None):
+    """Appends the new rows of a batch of requests to the cache: per-head
+    RMSNorm of q and k (where a weight is given), rotation at pos (None: the
+    row's index in its request; rope_base 0: none), k, v and the gate biases
+    logsigmoid(s) into the pages. k, v [rows, hkv, dh], q [rows, hq, dh] or
+    None, all possibly slices of one fused projection; cu_q [batch + 1],
+    kv_len [batch] (the new rows included) int32. Returns the rotated queries
+    [rows, hq, dh], or None without q."""
+    dev, dt, dh = cache.device, cache.dtype, cache.head_dim
+    rows, nb = k.shape[0], cache.batch
+    k_st = _rows3(k, rows, cache.n_heads_kv, dh, dt, dev, "k")
+    v_st = _rows3(v, rows, cache.n_heads_kv, dh, dt, dev, "v")
+    hq = q_st = 0
+    if q is not None:
+        hq = q.shape[1]
+        q_st = _rows3(q, rows, hq, dh, dt, dev, "q")
+        if q_out is None:
+            q_out = torch.empty((rows, hq, dh), dtype=dt, device=dev)
+        else:
+            _need(q_out.shape == (rows, hq, dh) and q_out.dtype == dt and q_out.device == dev
+                  and q_out.is_contiguous(), "q_out must be contiguous, as q in shape and dtype")
+    else:
+        _need(q_out is None, "q_out without q")
+    f32 = torch.float32
+    with _on(dev):
+        _check(_paged_append(
+            cache._ref, None if q is None else q.data_ptr(), q_st, k.data_ptr(), k_st,
+            v.data_ptr(), v_st, rows, _vec(cu_q, nb + 1, torch.int32, dev, "cu_q"),
+            _vec(kv_len, nb, torch.int32, dev, "kv_len"), nb, hq,
+            _vec(pos, rows, torch.int32, dev, "pos"), _vec(s, rows, f32, dev, "s"),
+            _vec(q_norm, dh, f32, dev, "q_norm"), _vec(k_norm, dh, f32, dev, "k_norm"), eps,
+            rope_base, None if q_out is None else q_out.data_ptr(), _stream(stream, dev)),
+            "tg_paged_append")
+    return q_out
+
+
+def tg_paged_attn(cache: PagedKV, q, cu_q, kv_len, gain=None, tau=None,
+                  max_kv: Optional[int] = None, out=None, lse=None, ws=None, stream=None):
+    """Token-gated attention of a batch of chunks of new tokens over the paged
+    cache, which holds their own rows already (tg_paged_append). q [rows, hq,
+    dh] rotated; gain, tau [hq] fp32; max_kv: an upper bound of kv_len (None:
+    the table's capacity). lse [hq, rows] fp32 is written when given. Returns
+    out [rows, hq, dh]."""
+    dev, dt, dh = cache.device, cache.dtype, cache.head_dim
+    rows, hq, nb = q.shape[0], q.shape[1], cache.batch
+    q_st = _rows3(q, rows, hq, dh, dt, dev, "q")
+    if out is None:
+        out = torch.empty((rows, hq, dh), dtype=dt, device=dev)
+    else:
+        _need(out.shape == (rows, hq, dh) and out.dtype == dt and out.device == dev
+              and out.is_contiguous(), "out must be contiguous, as q in shape and dtype")
+    need = tg_workspace_size(TG_OP_PAGED_ATTN, n=nb, k=rows, n_heads_q=hq,
+                             n_heads_kv=cache.n_heads_kv, head_dim=dh, dtype=cache.c.dtype)
+    ws = _ws(need, dev, ws)
+    f32 = torch.float32
+    with _on(dev):
+        _check(_paged_attn(
+            cache._ref, q.data_ptr(), q_st, rows, _vec(cu_q, nb + 1, torch.int32, dev, "cu_q"),
+            _vec(kv_len, nb, torch.int32, dev, "kv_len"), nb, hq,
+            cache.capacity if max_kv is None else int(max_kv), _vec(gain, hq, f32, dev, "gain"),
+            _vec(tau, hq, f32, dev, "tau"), out.data_ptr(), _vec(lse, hq * rows, f32, dev, "lse"),
+            ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream, dev)),
+            "tg_paged_attn")
+    return out
+
+
+# ----------------------------------------------------------------- 8-bit projections
+
+
+def tg_quantize_rows(x, xq=None, scale=None, stream=None):
+    """Rows of x [rows, cols] (bf16 or fp32, cols % 16 == 0) as 8-bit integers
+    with one scale each: (xq [rows, cols] int8, scale [rows] fp32)."""
+    rows, cols = x.shape
+    dev = x.device
+    _need(rows == 0 or cols <= 1 or x.stride(1) == 1, "x: each row must be contiguous")
+    if xq is None:
+        xq = torch.empty((rows, cols), dtype=torch.int8, device=dev)
+    else:
+        _need(xq.shape == x.shape and xq.dtype == torch.int8 and xq.device == dev
+              and xq.is_contiguous(), "xq must be contiguous int8 of x's shape")
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=dev)
+    with _on(dev):
+        _check(_quantize(x.data_ptr(), x.stride(0) if rows > 1 else cols, rows, cols, _dt(x),
+                         xq.data_ptr(), _vec(scale, rows, torch.float32, dev, "scale"),
+                         _stream(stream, dev)), "tg_quantize_rows")
+    return xq, scale
+
+
+def tg_linear_quantized(xq, xs, wq, ws, residual=None, y=None, dtype=torch.bfloat16, stream=None):
+    """y = (xq . wq^T) * xs[:, None] * ws (+ residual): xq [m, k], wq [n, k]
+    int8 with their scales xs [m], ws [n] fp32 (tg_quantize_rows); y and
+    residual [m, n] in dtype (bf16 or fp32)."""
+    m, k = xq.shape
+    n = wq.shape[0]
+    dev = xq.device
+    _need(wq.shape == (n, k) and xq.dtype == torch.int8 and wq.dtype == torch.int8
+          and wq.device == dev and xq.is_contiguous() and wq.is_contiguous(),
+          "xq [m, k] and wq [n, k] must be contiguous int8 on one device")
+    if y is None:
+        y = torch.empty((m, n), dtype=dtype, device=dev)
+    for name, t in (("y", y), ("residual", residual)):
+        _need(t is None or (t.shape == (m, n) and t.dtype == y.dtype and t.device == dev
+                            and t.is_contiguous()), f"{name} must be contiguous [m, n], as y")
+    with _on(dev):
+        _check(_linear_q(xq.data_ptr(), _vec(xs, m, torch.float32, dev, "xs"), wq.data_ptr(),
+                         _vec(ws, n, torch.float32, dev, "ws"),
+                         None if residual is None else residual.data_ptr(), m, n, k, _dt(y),
+                         y.data_ptr(), _stream(stream, dev)), "tg_linear_quantized")
+    return y
+
+
 __all__ = [
     "tg_score", "tg_linear", "tg_fold_norm_weight", "tg_prefill_host", "tg_topk_select", "tg_topk_select_noalloc", "SELECT_NOALLOC_MAX_N", "tg_compact", "tg_gated_attn_prefill", "tg_gated_attn_forward", "tg_gated_attn_backward", "tg_prefill", "tg_prefill_multi", "tg_prefill_batch", "tg_decode_step",
     "tg_workspace_size", "tg_status_string", "tg_device_error", "tg_version", "Model",
@@ -658,4 +879,6 @@ __all__ = [
     "TG_ERR_BUDGET", "TG_ERR_WORKSPACE", "TG_ERR_CUDA", "TG_F32", "TG_BF16", "TG_OP_SCORE",
     "TG_OP_TOPK_SELECT", "TG_OP_COMPACT", "TG_OP_GATED_ATTN", "TG_OP_PREFILL", "TG_OP_DECODE",
     "TG_OP_GATED_ATTN_BWD", "GdnLayer", "tg_gated_deltanet", "tg_gated_deltanet_workspace_size",
+    "PagedKV", "tg_paged_append", "tg_paged_attn", "tg_quantize_rows", "tg_linear_quantized",
+    "TG_OP_PAGED_ATTN",
 ]

@@ -1,0 +1,438 @@
+// k_paged.cu -- the paged key/value cache of a serving process: appending new
+// rows to it (tg_paged_append) and the CUDA-core attention over it
+// (tg_paged_attn, fp32).
+//
+// The cache is a pool of pages of page_size rows; request b's row j sits in
+// page table[b][j / page_size], row j % page_size. Layers above the gate hold
+// the kept tokens' rows with their gate bias logsigmoid(s_j), layers at or
+// below it every row; generated rows have bias 0 (Tencent Cloud article
+// "TokenGate：端到端可训练的 Token 剪枝机制，让大模型 Prefill 提速 11.3 倍", sections
+// "TokenGate 提前筛选 Token" and "TokenGate 的工程验证仍有限": generated tokens are
+// never pruned, and the bias fixed at prefill acts as an additive mask).
+//
+// Lengths, chunk offsets, positions and page numbers are device data: they are
+// checked where they are used, and a row or page out of range is skipped and
+// reported in the device error word.
+#include "tg_device.cuh"
+#include "tg_internal.h"
+#include "tg_paged.cuh"
+
+namespace tg {
+namespace {
+
+__device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
+  const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = __bfloat1622float2(e[i]);
+    f[2 * i] = t.x;
+    f[2 * i + 1] = t.y;
+  }
+}
+__device__ __forceinline__ void unpack(const uint4& u, float (&f)[4]) {
+  f[0] = __uint_as_float(u.x);
+  f[1] = __uint_as_float(u.y);
+  f[2] = __uint_as_float(u.z);
+  f[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ uint4 repack(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ uint4 repack(const float (&f)[4]) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                    __float_as_uint(f[3]));
+}
+
+// ---------------------------------------------------------------- append
+// y = x / sqrt(mean(x^2) + eps) * w per head (when a weight is given), then
+// the rotate-half rotation by pos * theta_i; q to q_out, k and v to their
+// pages, bias = logsigmoid(s). Bound by HBM: every row in once, out once.
+// One head is held by dh / 2 / kVec lanes (8 lanes of bf16 at dh 128), each
+// with one 16-byte vector of the first half and the matching one of the
+// second, so that rotation pairs meet in one thread and the norm needs three
+// shuffles. A CTA takes `tok` tokens: their angles (fp64, from the host's
+// theta_i, so that no thread evaluates a power) go to shared memory first.
+constexpr int kAppThreads = 256;
+
+template <typename T, int kDh>
+__global__ void __launch_bounds__(kAppThreads) paged_append(const __grid_constant__ PagedAppendArgs a,
+                                                            int tok) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int kHalf = kDh / 2;
+  constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+  constexpr int kLanes = kHalf / kVec;           // lanes of one head
+  constexpr int kHeads = kAppThreads / kLanes;   // heads of one pass
+  constexpr int kMaxTok = kAppThreads / kHalf;
+  __shared__ __align__(16) float s_cos[kMaxTok][kHalf];
+  __shared__ __align__(16) float s_sin[kMaxTok][kHalf];
+  __shared__ int64_t s_dst_page[kMaxTok];  // page of the token's row, or -1 (skip)
+  __shared__ int s_dst_row[kMaxTok];
+  __shared__ int s_req[kMaxTok];
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tok;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(tok), a.rows - t0));
+  if (threadIdx.x < kMaxTok) s_req[threadIdx.x] = 0;
+  __syncthreads();
+  // request of each token: the number of requests that end at or before it
+  // (cu_q ascends), counted by all threads at once
+  for (int b = threadIdx.x; b < a.batch; b += kAppThreads) {
+    const int64_t end = __ldg(a.cu_q + b + 1);
+    for (int i = 0; i < nt; ++i)
+      if (end <= t0 + i) atomicAdd(&s_req[i], 1);
+  }
+  __syncthreads();
+  if (threadIdx.x < nt) {
+    const int i = threadIdx.x;
+    const int64_t t = t0 + i;
+    const int b = s_req[i];
+    int64_t page = -1;
+    int row = 0;
+    bool bad = false;
+    if (b < a.batch) {  // rows behind the last request are left alone
+      const int64_t lo = __ldg(a.cu_q + b), hi = __ldg(a.cu_q + b + 1);
+      const int64_t dst = static_cast<int64_t>(__ldg(a.kv_len + b)) - (hi - lo) + (t - lo);
+      const int64_t blk = dst / a.kv.page_size;
+      bad = lo > t || dst < 0 || blk >= a.kv.table_stride;
+      if (!bad) {
+        page = __ldg(a.kv.table + static_cast<int64_t>(b) * a.kv.table_stride + blk);
+        row = static_cast<int>(dst % a.kv.page_size);
+        bad = page < 0 || page >= a.kv.n_pages;
+      }
+    }
+    if (bad) {
+      page = -1;
+      report_error(a.err, kErrIndexRange);
+    }
+    s_dst_page[i] = page;
+    s_dst_row[i] = row;
+    if (page >= 0 && a.kv.bias != nullptr)
+      a.kv.bias[page * a.kv.bias_page_stride + row] = a.s ? logsigmoid_f(__ldg(a.s + t)) : 0.0f;
+  }
+  if (a.rotate) {
+    for (int e = threadIdx.x; e < nt * kHalf; e += kAppThreads) {
+      const int i = e / kHalf, f = e % kHalf;
+      int64_t pos;
+      if (a.pos != nullptr) {
+        pos = __ldg(a.pos + t0 + i);
+      } else {  // the row's index in its request
+        const int b = s_req[i];
+        const int64_t t = t0 + i;
+        pos = b < a.batch ? static_cast<int64_t>(__ldg(a.kv_len + b)) - __ldg(a.cu_q + b + 1) + t : 0;
+      }
+      const float2 cs = rope_cos_sin_theta(pos, a.theta[f]);
+      s_cos[i][f] = cs.x;
+      s_sin[i][f] = cs.y;
+    }
+  }
+  __syncthreads();
+  const int sub = threadIdx.x % kLanes;
+  const int heads = a.hq + 2 * a.kv.hkv;
+  const int d0 = sub * kVec;
+  for (int i = 0; i < nt; ++i) {
+    if (s_req[i] >= a.batch) continue;
+    const int64_t t = t0 + i;
+    const int64_t page = s_dst_page[i];
+    const int row = s_dst_row[i];
+    for (int h0 = threadIdx.x / kLanes; h0 < ((heads + kHeads - 1) / kHeads) * kHeads; h0 += kHeads) {
+      const bool on = h0 < heads;  // every lane of the warp reaches the shuffles
+      const int kind = h0 < a.hq ? 0 : (h0 < a.hq + a.kv.hkv ? 1 : 2);
+      const int h = kind == 0 ? h0 : (kind == 1 ? h0 - a.hq : h0 - a.hq - a.kv.hkv);
+      const T* src = nullptr;
+      T* dst = nullptr;
+      if (on && kind == 0) {
+        src = static_cast<const T*>(a.q) + t * a.q_stride + h * kDh;
+        dst = static_cast<T*>(a.q_out) + (t * a.hq + h) * kDh;
+      } else if (on && page >= 0) {
+        src = static_cast<const T*>(kind == 1 ? a.k : a.v) + t * (kind == 1 ? a.k_stride : a.v_stride) +
+              h * kDh;
+        dst = static_cast<T*>(kind == 1 ? a.kv.k : a.kv.v) +
+              page * (kind == 1 ? a.kv.k_page_stride : a.kv.v_page_stride) +
+              (static_cast<int64_t>(row) * a.kv.hkv + h) * kDh;
+      }
+      uint4 ulo = make_uint4(0, 0, 0, 0), uhi = ulo;
+      if (src != nullptr) {
+        ulo = *reinterpret_cast<const uint4*>(src + d0);
+        uhi = *reinterpret_cast<const uint4*>(src + kHalf + d0);
+      }
+      const float* nw = kind == 0 ? a.q_norm : (kind == 1 ? a.k_norm : nullptr);
+      if (a.q_norm != nullptr || a.k_norm != nullptr || a.rotate) {
+        float lo[kVec], hi[kVec];
+        unpack(ulo, lo);
+        unpack(uhi, hi);
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) ss += lo[e] * lo[e] + hi[e] * hi[e];
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        if (nw != nullptr) {
+          const float r = rsqrtf(ss * (1.0f / kDh) + a.eps);
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) {
+            lo[e] = lo[e] * r * __ldg(nw + d0 + e);
+            hi[e] = hi[e] * r * __ldg(nw + kHalf + d0 + e);
+          }
+        }
+        if (kind < 2) {
+          if (a.rotate) {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+              const float c = s_cos[i][d0 + e], s = s_sin[i][d0 + e];
+              const float x = lo[e], y = hi[e];
+              lo[e] = x * c - y * s;
+              hi[e] = y * c + x * s;
+            }
+          }
+          ulo = repack(lo);
+          uhi = repack(hi);
+        }
+      }
+      if (dst != nullptr) {
+        *reinterpret_cast<uint4*>(dst + d0) = ulo;
+        *reinterpret_cast<uint4*>(dst + kHalf + d0) = uhi;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- attention, CUDA cores
+// One CTA per (32 rows of a request and KV head, KV head); a row is a (token,
+// query head of the group) pair, token-major, so that the keys are read once
+// for the whole group. Keys go through shared memory 32 at a time; thread
+// (ty, tx) holds rows 2 ty, 2 ty + 1 and keys tx + 8 i in the logits, columns
+// 4 tx + 32 c in the outputs, and the running maximum and sum of its two rows
+// (equal in the eight lanes of a row). All in fp32: the fp32 block's parity
+// needs full-precision products, which no tensor-core type gives.
+constexpr int kSimtRows = 32, kSimtKeys = 32, kSimtThreads = 128;
+
+template <typename T, int kDh>
+struct SimtSmem {
+  float q[kSimtRows][kDh + 4];
+  float k[kSimtKeys][kDh + 4];
+  float v[kSimtKeys][kDh];
+  float p[kSimtRows][kSimtKeys + 1];
+  float bias[kSimtKeys];
+};
+
+template <typename T, int kDh>
+__global__ void __launch_bounds__(kSimtThreads)
+    paged_attn_simt(const __grid_constant__ PagedAttnArgs a) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  SimtSmem<T, kDh>& sm = *reinterpret_cast<SimtSmem<T, kDh>*>(smem_raw);
+  __shared__ PagedTile s_tile;
+  pdl_trigger();
+  pdl_wait();
+  constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+  constexpr int kCols = kDh / 32;  // float4 columns of a thread's outputs
+  const int group = a.hq / a.kv.hkv;
+  const int g = blockIdx.y;
+  if (threadIdx.x < 32) {
+    const PagedTile t = find_tile(a, kSimtRows, blockIdx.x);
+    if (threadIdx.x == 0) s_tile = t;
+  }
+  __syncthreads();
+  const PagedTile tile = s_tile;
+  if (tile.req < 0) return;
+  const int tid = threadIdx.x, tx = tid & 7, ty = tid >> 3;
+  // rows of the tile: token (row0 + r) / group of the request, head (row0 + r) % group
+  const int n_rows = static_cast<int>(min(static_cast<int64_t>(kSimtRows), tile.n * group - tile.row0));
+  for (int e = tid; e < kSimtRows * (kDh / kVec); e += kSimtThreads) {
+    const int r = e / (kDh / kVec), c = (e % (kDh / kVec)) * kVec;
+    float f[kVec];
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (r < n_rows) {
+      const int64_t rr = tile.row0 + r;
+      u = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
+                                          (tile.tok0 + rr / group) * a.q_stride +
+                                          (g * group + rr % group) * kDh + c);
+    }
+    unpack(u, f);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) sm.q[r][c + i] = f[i];
+  }
+  float scale[2], gain[2];
+  int64_t limit[2];  // keys that the row sees
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 2 * ty + i;
+    const int64_t rr = tile.row0 + r;
+    const int h = g * group + static_cast<int>(rr % group);
+    scale[i] = kLog2e / (sqrtf(static_cast<float>(kDh)) * (a.tau ? __ldg(a.tau + h) : 1.0f));
+    gain[i] = a.gain && a.kv.bias ? __ldg(a.gain + h) * kLog2e : 0.0f;
+    limit[i] = r < n_rows ? tile.past + rr / group + 1 : 0;
+  }
+  const int64_t kv_end = tile.past + (tile.row0 + n_rows - 1) / group + 1;  // last row's limit
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float4 o[2][kCols];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+
+  for (int64_t kv0 = 0; kv0 < kv_end; kv0 += kSimtKeys) {
+    __syncthreads();  // the last tile's keys are read
+    for (int e = tid; e < kSimtKeys * (kDh / kVec); e += kSimtThreads) {
+      const int r = e / (kDh / kVec), c = (e % (kDh / kVec)) * kVec;
+      const int64_t j = kv0 + r;
+      float fk[kVec], fv[kVec];
+      uint4 uk = make_uint4(0, 0, 0, 0), uv = uk;
+      float b = 0.f;
+      if (j < kv_end) {
+        const int64_t page = page_of(a, tile.req, j);
+        if (page >= 0) {
+          const int64_t off = ((j % a.kv.page_size) * a.kv.hkv + g) * kDh + c;
+          uk = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.kv.k) +
+                                               page * a.kv.k_page_stride + off);
+          uv = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.kv.v) +
+                                               page * a.kv.v_page_stride + off);
+          if (c == 0 && a.kv.bias)
+            b = key_bias(a.kv.bias[page * a.kv.bias_page_stride + j % a.kv.page_size]);
+        }
+      }
+      unpack(uk, fk);
+      unpack(uv, fv);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        sm.k[r][c + i] = fk[i];
+        sm.v[r][c + i] = fv[i];
+      }
+      if (c == 0) sm.bias[r] = b;
+    }
+    __syncthreads();
+    float s[2][4] = {};
+#pragma unroll 4
+    for (int d = 0; d < kDh; d += 4) {
+      const float4 q0 = *reinterpret_cast<const float4*>(&sm.q[2 * ty][d]);
+      const float4 q1 = *reinterpret_cast<const float4*>(&sm.q[2 * ty + 1][d]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 kk = *reinterpret_cast<const float4*>(&sm.k[tx + 8 * i][d]);
+        s[0][i] += q0.x * kk.x + q0.y * kk.y + q0.z * kk.z + q0.w * kk.w;
+        s[1][i] += q1.x * kk.x + q1.y * kk.y + q1.z * kk.z + q1.w * kk.w;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float z = s[r][i] * scale[r] + gain[r] * sm.bias[tx + 8 * i];
+        s[r][i] = kv0 + tx + 8 * i < limit[r] && !(z <= kMaskedLogit) ? z : -INFINITY;
+        mx = fmaxf(mx, s[r][i]);
+      }
+#pragma unroll
+      for (int w = 4; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, w));
+      const float m_new = fmaxf(m[r], mx);
+      const float m_use = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet: all weights 0
+      const float corr = exp2f(m[r] - m_use);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float w = exp2f(s[r][i] - m_use);
+        sm.p[2 * ty + r][tx + 8 * i] = w;
+        sum += w;
+      }
+#pragma unroll
+      for (int w = 4; w > 0; w >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, w);
+      l[r] = l[r] * corr + sum;
+      m[r] = m_new;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        o[r][c].x *= corr;
+        o[r][c].y *= corr;
+        o[r][c].z *= corr;
+        o[r][c].w *= corr;
+      }
+    }
+    __syncwarp();  // a row's weights are written and read by one warp
+    // keys that only some rows see are skipped by the others (not weighted
+    // with zero: a value that a row must not see may be infinite or NaN)
+    const bool some = kv0 + kSimtKeys > limit[0] || kv0 + kSimtKeys > limit[1];
+#pragma unroll 2
+    for (int j = 0; j < kSimtKeys; ++j) {
+      const float p0 = sm.p[2 * ty][j], p1 = sm.p[2 * ty + 1][j];
+      const bool see0 = !some || kv0 + j < limit[0], see1 = !some || kv0 + j < limit[1];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        const float4 vv = *reinterpret_cast<const float4*>(&sm.v[j][4 * tx + 32 * c]);
+        if (see0) {
+          o[0][c].x = fmaf(p0, vv.x, o[0][c].x);
+          o[0][c].y = fmaf(p0, vv.y, o[0][c].y);
+          o[0][c].z = fmaf(p0, vv.z, o[0][c].z);
+          o[0][c].w = fmaf(p0, vv.w, o[0][c].w);
+        }
+        if (see1) {
+          o[1][c].x = fmaf(p1, vv.x, o[1][c].x);
+          o[1][c].y = fmaf(p1, vv.y, o[1][c].y);
+          o[1][c].z = fmaf(p1, vv.z, o[1][c].z);
+          o[1][c].w = fmaf(p1, vv.w, o[1][c].w);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    if (2 * ty + r >= n_rows) continue;
+    const int64_t rr = tile.row0 + 2 * ty + r;
+    const int64_t t = tile.tok0 + rr / group;
+    const int h = g * group + static_cast<int>(rr % group);
+    const bool any = l[r] != 0.f;  // a row that sees nothing is zero
+    const float inv = any ? 1.0f / l[r] : 0.f;
+    if (a.lse != nullptr && tx == 0)
+      a.lse[h * a.rows + t] = any ? (m[r] + log2f(l[r])) * kLn2 : -INFINITY;
+    T* out = static_cast<T*>(a.out) + (t * a.hq + h) * kDh;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      const float f[4] = {o[r][c].x * inv, o[r][c].y * inv, o[r][c].z * inv, o[r][c].w * inv};
+      if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(out + 4 * tx + 32 * c) = make_float4(f[0], f[1], f[2], f[3]);
+      } else {
+        *reinterpret_cast<uint2*>(out + 4 * tx + 32 * c) =
+            make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+      }
+    }
+  }
+}
+
+template <typename T, int kDh>
+cudaError_t run_append(const PagedAppendArgs& a, cudaStream_t st) {
+  constexpr int kMaxTok = kAppThreads / (kDh / 2);
+  // one token per CTA until every SM has several CTAs, then as many as one
+  // pass of angles covers
+  int tok = 1;
+  while (tok < kMaxTok && a.rows / (2 * tok) >= 8 * num_sms()) tok *= 2;
+  const unsigned grid = static_cast<unsigned>((a.rows + tok - 1) / tok);
+  TG_CUDA_TRY(launch_pdl(paged_append<T, kDh>, dim3(grid), dim3(kAppThreads), 0, st, a, tok));
+  return cudaGetLastError();
+}
+
+template <typename T, int kDh>
+cudaError_t run_simt(const PagedAttnArgs& a, cudaStream_t st) {
+  const int group = a.hq / a.kv.hkv;
+  // an upper bound of the row tiles: each request's last one may be short
+  const int64_t tiles = a.rows * group / kSimtRows + (a.batch < a.rows ? a.batch : a.rows);
+  constexpr int kBytes = static_cast<int>(sizeof(SimtSmem<T, kDh>));
+  auto kern = paged_attn_simt<T, kDh>;
+  TG_CUDA_TRY(set_smem_attr_once(reinterpret_cast<const void*>(kern), kBytes));
+  TG_CUDA_TRY(launch_pdl(kern, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.kv.hkv)),
+                         dim3(kSimtThreads), kBytes, st, a));
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedAppendArgs& a, bool bf16, cudaStream_t st) {
+  if (a.rows <= 0 || a.batch <= 0) return cudaSuccess;
+  if (bf16)
+    return a.kv.dh == 128 ? run_append<__nv_bfloat16, 128>(a, st) : run_append<__nv_bfloat16, 64>(a, st);
+  return a.kv.dh == 128 ? run_append<float, 128>(a, st) : run_append<float, 64>(a, st);
+}
+
+cudaError_t launch_paged_attn_simt(const PagedAttnArgs& a, bool bf16, cudaStream_t st) {
+  if (a.rows <= 0 || a.batch <= 0) return cudaSuccess;
+  if (bf16)
+    return a.kv.dh == 128 ? run_simt<__nv_bfloat16, 128>(a, st) : run_simt<__nv_bfloat16, 64>(a, st);
+  return a.kv.dh == 128 ? run_simt<float, 128>(a, st) : run_simt<float, 64>(a, st);
+}
+
+}  // namespace tg

@@ -973,6 +973,8 @@ size_t tg_workspace_size(tg_op op, const tg_shape* s) {
       m.d_ffn = s->d_ffn;
       return DecodePlan(nullptr, m, s->k).bytes;
     }
+    case TG_OP_PAGED_ATTN:
+      return 0;
   }
   return 0;
 }
@@ -1915,13 +1917,174 @@ tg_status tg_gated_deltanet(const tg_gdn_layer* L, const void* qkv, const void* 
   return TG_OK;
 }
 
+}  // extern "C"
+
+// ------------------------------------------------------------------ paged cache
+namespace {
+bool mult16(int64_t elems, tg_dtype dt) { return elems * int64_t(elem_size(dt)) % 16 == 0; }
+
+// Checks shared by the calls on a paged cache; fills the kernels' view of it.
+tg_status paged_view(const tg_paged_kv* c, const int32_t* cu_q, const int32_t* kv_len, int64_t rows,
+                     int32_t batch, PagedKv* v) {
+  TG_CHECK(c != nullptr, TG_ERR_INVALID_ARG);
+  TG_CHECK(c->dtype == TG_BF16 || c->dtype == TG_F32, TG_ERR_UNSUPPORTED);
+  TG_CHECK(c->head_dim == 64 || c->head_dim == 128, TG_ERR_UNSUPPORTED);
+  const int ps = c->page_size;
+  TG_CHECK(ps == 16 || ps == 32 || ps == 64 || ps == 128 || ps == 256, TG_ERR_UNSUPPORTED);
+  TG_CHECK(rows >= 0 && rows < (int64_t(1) << 31) && batch >= 0, TG_ERR_INVALID_ARG);
+  // a call without rows has nothing to point at
+  TG_CHECK(rows == 0 || batch == 0 || (c->k && c->v && c->table && cu_q && kv_len),
+           TG_ERR_INVALID_ARG);
+  TG_CHECK(c->n_pages >= 1 && c->n_pages < (int64_t(1) << 31) && c->table_stride >= 1 &&
+               c->n_heads_kv >= 1 && c->n_heads_kv <= 65535,
+           TG_ERR_INVALID_ARG);
+  const int64_t page = int64_t(ps) * c->n_heads_kv * c->head_dim;
+  TG_CHECK(c->k_page_stride >= page && c->v_page_stride >= page, TG_ERR_INVALID_ARG);
+  TG_CHECK(mult16(c->k_page_stride, c->dtype) && mult16(c->v_page_stride, c->dtype) &&
+               aligned16(c->k) && aligned16(c->v),
+           TG_ERR_INVALID_ARG);
+  TG_CHECK(c->bias == nullptr || c->bias_page_stride >= ps, TG_ERR_INVALID_ARG);
+  *v = PagedKv{c->k, c->v, c->bias, c->table, c->n_pages, c->k_page_stride, c->v_page_stride,
+               c->bias_page_stride, c->table_stride, ps, c->n_heads_kv, c->head_dim};
+  return TG_OK;
+}
+}  // namespace
+
+extern "C" {
+
+tg_status tg_paged_append(const tg_paged_kv* cache, const void* q, int64_t q_stride, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, int64_t rows,
+                          const int32_t* cu_q, const int32_t* kv_len, int32_t batch, int32_t hq,
+                          const int32_t* pos, const float* s, const float* q_norm,
+                          const float* k_norm, float eps, float rope_base, void* q_out,
+                          tg_stream stream) {
+  PagedAppendArgs a{};
+  const tg_status e = paged_view(cache, cu_q, kv_len, rows, batch, &a.kv);
+  if (e != TG_OK) return e;
+  const tg_dtype dt = cache->dtype;
+  const int dh = cache->head_dim, hkv = cache->n_heads_kv;
+  const bool none = rows == 0 || batch == 0;
+  TG_CHECK((none || (k && v)) && k_stride >= int64_t(hkv) * dh && v_stride >= int64_t(hkv) * dh &&
+               mult16(k_stride, dt) && mult16(v_stride, dt) && aligned16(k) && aligned16(v),
+           TG_ERR_INVALID_ARG);
+  if (none) {
+    TG_CHECK(hq >= 0, TG_ERR_INVALID_ARG);
+  } else if (q != nullptr) {
+    TG_CHECK(hq >= 1 && hq <= 65535 && q_out != nullptr && q_stride >= int64_t(hq) * dh &&
+                 mult16(q_stride, dt) && aligned16(q) && aligned16(q_out),
+             TG_ERR_INVALID_ARG);
+    TG_CHECK(q != q_out || q_stride == int64_t(hq) * dh, TG_ERR_INVALID_ARG);
+  } else {
+    TG_CHECK(hq == 0 && q_out == nullptr, TG_ERR_INVALID_ARG);
+  }
+  TG_CHECK(rope_base >= 0.f && std::isfinite(rope_base), TG_ERR_INVALID_ARG);
+  TG_CHECK(eps >= 0.f || (q_norm == nullptr && k_norm == nullptr), TG_ERR_INVALID_ARG);
+  if (none) return TG_OK;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.rows = rows;
+  a.cu_q = cu_q;
+  a.kv_len = kv_len;
+  a.batch = batch;
+  a.hq = hq;
+  a.pos = pos;
+  a.s = s;
+  a.q_norm = q != nullptr ? q_norm : nullptr;
+  a.k_norm = k_norm;
+  a.eps = eps;
+  a.rotate = rope_base > 0.f;
+  a.q_out = q_out;
+  for (int i = 0; a.rotate && i < dh / 2; ++i)
+    a.theta[i] = std::exp2(-(2.0 * i / dh) * std::log2(static_cast<double>(rope_base)));
+  a.err = device_error_word();
+  const double bytes = 2.0 * rows * (hq + 2 * hkv) * dh * double(elem_size(dt));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(traced(TG_K_PAGED_APPEND, rows, 0.0, bytes, st, [&] {
+    return launch_paged_append(a, dt == TG_BF16, st);
+  }));
+}
+
+tg_status tg_paged_attn(const tg_paged_kv* cache, const void* q, int64_t q_stride, int64_t rows,
+                        const int32_t* cu_q, const int32_t* kv_len, int32_t batch, int32_t hq,
+                        int64_t max_kv, const float* gain, const float* tau, void* out, float* lse,
+                        void* ws, size_t ws_bytes, tg_stream stream) {
+  PagedAttnArgs a{};
+  const tg_status e = paged_view(cache, cu_q, kv_len, rows, batch, &a.kv);
+  if (e != TG_OK) return e;
+  const tg_dtype dt = cache->dtype;
+  const int dh = cache->head_dim, hkv = cache->n_heads_kv;
+  const bool none = rows == 0 || batch == 0;
+  TG_CHECK((none || (q && out)) && hq >= 1 && hq <= 65535 && hq % hkv == 0, TG_ERR_INVALID_ARG);
+  TG_CHECK(q_stride >= int64_t(hq) * dh && mult16(q_stride, dt) && aligned16(q) && aligned16(out),
+           TG_ERR_INVALID_ARG);
+  TG_CHECK(max_kv >= 1 && max_kv <= int64_t(cache->table_stride) * cache->page_size,
+           TG_ERR_INVALID_ARG);
+  if (none) return TG_OK;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.rows = rows;
+  a.cu_q = cu_q;
+  a.kv_len = kv_len;
+  a.batch = batch;
+  a.hq = hq;
+  a.max_kv = max_kv;
+  a.gain = gain;
+  a.tau = tau;
+  a.out = out;
+  a.lse = lse;
+  a.err = device_error_word();
+  (void)ws;
+  (void)ws_bytes;
+  const double bytes = 2.0 * rows * hq * dh * double(elem_size(dt));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(traced(TG_K_PAGED_ATTN, rows, 0.0, bytes, st, [&] {
+    return launch_paged_attn_simt(a, dt == TG_BF16, st);
+  }));
+}
+
+// ------------------------------------------------------------------ 8-bit projections
+tg_status tg_quantize_rows(const void* x, int64_t x_stride, int64_t rows, int32_t cols, tg_dtype dt,
+                           int8_t* xq, float* scale, tg_stream stream) {
+  TG_CHECK(dt == TG_BF16 || dt == TG_F32, TG_ERR_UNSUPPORTED);
+  TG_CHECK((rows == 0 || (x && xq && scale)) && rows >= 0 && rows < (int64_t(1) << 31) && cols >= 1,
+           TG_ERR_INVALID_ARG);
+  TG_CHECK(cols % 16 == 0, TG_ERR_UNSUPPORTED);
+  TG_CHECK(x_stride >= cols && mult16(x_stride, dt) && aligned16(x) && aligned16(xq),
+           TG_ERR_INVALID_ARG);
+  const double bytes = rows * (double(cols) * (elem_size(dt) + 1) + 4);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(traced(TG_K_QUANTIZE, rows, 0.0, bytes, st, [&] {
+    return launch_quantize_rows(x, x_stride, rows, cols, dt == TG_BF16, xq, scale, st);
+  }));
+}
+
+tg_status tg_linear_quantized(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws,
+                              const void* residual, int64_t m, int32_t n, int32_t k, tg_dtype dt,
+                              void* y, tg_stream stream) {
+  TG_CHECK(dt == TG_BF16 || dt == TG_F32, TG_ERR_UNSUPPORTED);
+  TG_CHECK((m == 0 || (xq && xs && y)) && wq && ws && m >= 0 && m < (int64_t(1) << 31) && n >= 1 && k >= 1,
+           TG_ERR_INVALID_ARG);
+  TG_CHECK(n % 32 == 0 && k % 16 == 0 && k <= 131056, TG_ERR_UNSUPPORTED);
+  TG_CHECK(aligned16(xq) && aligned16(wq) && aligned16(y) && aligned16(residual),
+           TG_ERR_INVALID_ARG);
+  const QuantGemmArgs g{xq, xs, wq, ws, residual, y, m, n, k, dt == TG_BF16};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(traced(TG_K_GEMM_INT, m, 2.0 * m * n * k, 0.0, st, [&] {
+    return launch_quant_gemm(g, st);
+  }));
+}
+
 const char* tg_kernel_name(int32_t kernel) {
   static const char* names[TG_K_COUNT] = {
       "copy", "rmsnorm", "gemm_tc_store", "gemm_tc_residual", "gemm_tc_swiglu", "gemm_tc_score",
       "rope_prep", "attention_tc", "select", "compact", "gemm_f32", "attention_f32", "f32_helper",
       "gemm_tc_qkv", "rope_table", "decode_step", "attn_bwd_prep", "attn_bwd_dkdv",
       "attn_bwd_dq", "attn_bwd_final", "gdn_prep", "gdn_chunk", "gdn_recur", "gdn_out",
-      "fold_norm"};
+      "fold_norm", "paged_append", "paged_attn", "quantize", "gemm_int"};
   return (kernel >= 0 && kernel < TG_K_COUNT) ? names[kernel] : "unknown";
 }
 

@@ -513,15 +513,18 @@ __device__ __forceinline__ float ex2_approx(float x) {
 // (cos, sin) of RoPE frequency i (of dh/2) at position pos: theta_i =
 // base^(-2i/dh), the angle pos * theta_i formed in fp64 and reduced mod 2 pi
 // before the fp32 sin/cos, so large positions keep their accuracy. Every
-// kernel that rotates q or k takes its angles from here.
-__device__ __forceinline__ float2 rope_cos_sin(int64_t pos, int i, int dh, float base) {
-  const double theta = exp2(-(2.0 * i / dh) * log2(static_cast<double>(base)));
+// kernel that rotates q or k takes its angles from here (with a theta_i that
+// the host formed: rope_cos_sin_theta).
+__device__ __forceinline__ float2 rope_cos_sin_theta(int64_t pos, double theta) {
   const double ang = static_cast<double>(pos) * theta;
   const double two_pi = 6.283185307179586476925286766559;
   const double red = ang - two_pi * rint(ang * (1.0 / two_pi));
   float sv, cv;
   sincosf(static_cast<float>(red), &sv, &cv);
   return make_float2(cv, sv);
+}
+__device__ __forceinline__ float2 rope_cos_sin(int64_t pos, int i, int dh, float base) {
+  return rope_cos_sin_theta(pos, exp2(-(2.0 * i / dh) * log2(static_cast<double>(base))));
 }
 
 // 2^x for a pair, on the FMA pipe instead of the MUFU unit, for x <= 8:

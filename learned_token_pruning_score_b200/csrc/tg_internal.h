@@ -345,6 +345,63 @@ struct GdnArgs {
 // 3: gated output norm.
 cudaError_t launch_gdn(const GdnArgs& a, bool bf16, int stage, cudaStream_t st);
 
+// ---- paged key/value cache (k_paged.cu, k_paged_tc.cu)
+struct PagedKv {
+  void* k; void* v;                 // pages [n_pages][page_size, hkv, dh]
+  float* bias;                      // pages [n_pages][page_size] or null
+  const int32_t* table;             // [batch][table_stride] page of each block of page_size rows
+  int64_t n_pages;
+  int64_t k_page_stride, v_page_stride, bias_page_stride;  // elements between pages
+  int table_stride, page_size, hkv, dh;
+};
+struct PagedAppendArgs {
+  PagedKv kv;
+  const void* q; const void* k; const void* v;
+  int64_t q_stride, k_stride, v_stride;  // elements between tokens
+  int64_t rows;
+  const int32_t* cu_q;              // [batch + 1]
+  const int32_t* kv_len;            // [batch], the new rows included
+  int batch, hq;                    // hq 0: no queries
+  const int32_t* pos;               // [rows] or null: the row's index in its request
+  const float* s;                   // [rows] gate scores or null (bias 0)
+  const float* q_norm; const float* k_norm; float eps;
+  bool rotate;
+  void* q_out;                      // [rows, hq, dh]
+  unsigned int* err;
+  double theta[64];                 // base^(-2i/dh), i < dh / 2
+};
+cudaError_t launch_paged_append(const PagedAppendArgs& a, bool bf16, cudaStream_t st);
+
+struct PagedAttnArgs {
+  PagedKv kv;
+  const void* q; int64_t q_stride;  // [rows, hq, dh], elements between tokens
+  int64_t rows;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  int batch, hq;
+  int64_t max_kv;                   // no kv_len is above it
+  const float* gain; const float* tau;
+  void* out;                        // [rows, hq, dh]
+  float* lse;                       // [hq, rows] or null
+  unsigned int* err;
+};
+// CUDA cores, fp32 arithmetic
+cudaError_t launch_paged_attn_simt(const PagedAttnArgs& a, bool bf16, cudaStream_t st);
+
+// ---- 8-bit integers (k_quant.cu)
+// xq = rint(127 x / amax), scale = amax / 127 per row; cols % 16 == 0.
+cudaError_t launch_quantize_rows(const void* x, int64_t x_stride, int64_t rows, int cols, bool bf16,
+                                 int8_t* xq, float* scale, cudaStream_t st);
+struct QuantGemmArgs {
+  const int8_t* x; const float* xs;  // [m, k], [m]
+  const int8_t* w; const float* ws;  // [n, k], [n]
+  const void* residual;              // [m, n] or null; may be y
+  void* y;                           // [m, n]
+  int64_t m; int n, k;
+  bool bf16;                         // type of y and residual (else fp32)
+};
+cudaError_t launch_quant_gemm(const QuantGemmArgs& g, cudaStream_t st);
+
 // ---- tensor maps (tg_tmap.cu)
 // 2-D bf16 tensor map, row-major [rows, cols] with row stride ld (elements),
 // box [box_rows, 64 cols], 128-byte swizzle. Returns false on failure.
