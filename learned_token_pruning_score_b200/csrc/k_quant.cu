@@ -171,6 +171,8 @@ cudaError_t launch_quantize_rows(const void* x, int64_t x_stride, int64_t rows, 
 
 cudaError_t launch_quant_gemm(const QuantGemmArgs& g, cudaStream_t st) {
   if (g.m <= 0) return cudaSuccess;
+  if (g.m > 256) return launch_quant_gemm_wide(g, st);
+  if (g.m > 4) return launch_quant_gemm_narrow(g, st);
   const dim3 grid(static_cast<unsigned>((g.n + 8 * kGvCols - 1) / (8 * kGvCols)),
                   static_cast<unsigned>((g.m + kGvRows - 1) / kGvRows));
   if (g.bf16) TG_CUDA_TRY(launch_pdl(quant_gemv<__nv_bfloat16>, grid, dim3(256), 0, st, g));

@@ -1,0 +1,529 @@
+// k_quant_tc.cu -- the 8-bit projection product on the 5th-generation tensor
+// cores (sm_100a), tg_linear_quantized:
+//
+//   y[i, j] = (sum_k xq[i, k] wq[j, k]) xs[i] ws[j] (+ residual[i, j])
+//
+// tcgen05.mma kind::i8 (signed 8-bit operands, 32-bit integer accumulators in
+// TMEM): the sum is exact, so the order of its terms, and how it is split,
+// never changes a result. Both operands are K-major with 128-byte rows of 128
+// integers, swizzled, as TMA lays them down; columns past k and rows past m
+// or n are read as zeros.
+//
+// Two kernels, chosen by the rows of x:
+//   wide    persistent CTA pairs, 256 x 256 tiles (cta_group::2), for the
+//           chunks of a prefill: bound by the tensor pipe.
+//   narrow  up to 128 rows of x a tile: the weights are the M operand (128
+//           output channels a CTA), the rows of x the N operand, and a cluster
+//           of up to 8 CTAs splits k, so that a decoding batch's weights stream
+//           through every SM; the partial sums meet through distributed shared
+//           memory. Bound by HBM (each weight read once).
+#include <atomic>
+
+#include "tg_device.cuh"
+#include "tg_internal.h"
+
+namespace tg {
+namespace {
+
+// Instruction descriptor of tcgen05.mma kind::i8: signed 8-bit A and B (both
+// K-major), 32-bit integer accumulator, shape M x N.
+__host__ __device__ constexpr uint32_t idesc_s8_s32(int m, int n) {
+  return (2u << 4)                                   // accumulator format: s32
+         | (1u << 7)                                 // A format: s8
+         | (1u << 10)                                // B format: s8
+         | (static_cast<uint32_t>(n >> 3) << 17)     // N / 8
+         | (static_cast<uint32_t>(m >> 4) << 24);    // M / 16
+}
+
+__device__ __forceinline__ void umma_i8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_i8_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+constexpr int kBK = 128;       // integers (bytes) of k per stage: one swizzled row
+constexpr int kThreads = 256;
+
+struct Params {
+  int64_t m;
+  int n, k;
+  const float* xs;
+  const float* ws;
+  const void* residual;
+  void* y;
+  int tiles_m, tiles_n;
+  int stages;  // narrow
+  int cols;    // narrow: columns of the N operand (rows of x of a tile, padded to 16)
+  unsigned int* err;
+};
+
+// ------------------------------------------------------------------ wide
+// Structure and barriers are those of the bf16 GEMM's CTA pairs (k_gemm_tc.cu):
+//   warp 0 (both) TMA into a 6-stage ring of 32 KB (128 rows of x and 128 of w
+//   a CTA), warp 1 (rank 0) issues four MMAs of 256 x 256 x 32 a stage into one
+//   of two TMEM accumulators, warps 4-7 (both) scale and store the other one.
+struct Wide {
+  static constexpr int kHalfBytes = 128 * kBK;
+  static constexpr int kStageBytes = 2 * kHalfBytes;
+  static constexpr int kStages = 6;
+  static constexpr int kTmemCols = 512;
+  static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + 256;
+};
+
+// 32 accumulators of one row, scaled (and added to the residual), to y.
+template <typename T>
+__device__ __forceinline__ void store32(const Params& p, int64_t row, int col, float xs,
+                                        const uint32_t (&acc)[32]) {
+  float v[32];
+#pragma unroll
+  for (int j = 0; j < 32; j += 4) {
+    const float4 w = __ldg(reinterpret_cast<const float4*>(p.ws + col + j));
+    v[j] = static_cast<float>(static_cast<int>(acc[j])) * xs * w.x;
+    v[j + 1] = static_cast<float>(static_cast<int>(acc[j + 1])) * xs * w.y;
+    v[j + 2] = static_cast<float>(static_cast<int>(acc[j + 2])) * xs * w.z;
+    v[j + 3] = static_cast<float>(static_cast<int>(acc[j + 3])) * xs * w.w;
+  }
+  const int64_t at = row * p.n + col;
+  if constexpr (sizeof(T) == 4) {
+    const float4* r = reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + at);
+    float4* y = reinterpret_cast<float4*>(static_cast<float*>(p.y) + at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float4 o = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      if (p.residual != nullptr) {
+        const float4 t = r[j];
+        o.x += t.x;
+        o.y += t.y;
+        o.z += t.z;
+        o.w += t.w;
+      }
+      y[j] = o;
+    }
+  } else {
+    const uint4* r = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + at);
+    uint4* y = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + at);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (p.residual != nullptr) {
+        const uint4 t = r[j];
+        const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __bfloat1622float2(e[i]);
+          v[8 * j + 2 * i] += f.x;
+          v[8 * j + 2 * i + 1] += f.y;
+        }
+      }
+      y[j] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                        pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+    }
+  }
+}
+
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    gemm_i8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                 const __grid_constant__ Params p) {
+  using C = Wide;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_addr(smem_raw);
+  uint8_t* tiles = smem_raw + ((1024 - (raw_addr & 1023)) & 1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(tiles + size_t(C::kStages) * C::kStageBytes);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* acc_full = empty + C::kStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_empty[a], 8);  // rank 0: 4 epilogue warps x 2 CTAs
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmW);
+  }
+  if (warp == 2) tmem_alloc_pair(tmem_slot, C::kTmemCols);
+  tc_fence_before();
+  cluster_sync();  // barriers of both CTAs initialised before any remote use
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+  const int num_tiles = p.tiles_m * p.tiles_n;
+  const int num_kb = (p.k + kBK - 1) / kBK;
+  const int pair = static_cast<int>(blockIdx.x >> 1), n_pairs = static_cast<int>(gridDim.x >> 1);
+
+  if (warp == 0 && lane == 0) {
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int tile = pair; tile < num_tiles && ok; tile += n_pairs) {
+      const int mb = tile / p.tiles_n, nb = tile % p.tiles_n;
+      const int x_row = mb * 256 + static_cast<int>(rank) * 128;
+      const int w_row = nb * 256 + static_cast<int>(rank) * 128;
+      for (int kb = 0; kb < num_kb; ++kb) {
+        if (!mbar_wait(&empty[s], ph ^ 1u, p.err)) { ok = false; break; }
+        uint8_t* dst = tiles + size_t(s) * C::kStageBytes;
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
+        const uint32_t bar = mapa_shared(smem_addr(&full[s]), 0);
+        tma_load_2d_pair(&tmX, bar, dst, kb * kBK, x_row);
+        tma_load_2d_pair(&tmW, bar, dst + C::kHalfBytes, kb * kBK, w_row);
+        if (++s == C::kStages) { s = 0; ph ^= 1u; }
+      }
+    }
+    // Every stage this CTA filled is released (by a commit that writes into
+    // this CTA's shared memory) before the CTA may exit.
+    for (int i = 0; i < C::kStages && ok; ++i) {
+      if (!mbar_wait(&empty[s], ph ^ 1u, p.err)) break;
+      if (++s == C::kStages) { s = 0; ph ^= 1u; }
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    constexpr uint32_t idesc = idesc_s8_s32(256, 256);
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    int it = 0;
+    for (int tile = pair; tile < num_tiles && ok; tile += n_pairs, ++it) {
+      const int a = it & 1;
+      if (!mbar_wait(&acc_empty[a], (static_cast<uint32_t>(it >> 1) & 1u) ^ 1u, p.err)) break;
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(a * 256);
+      for (int kb = 0; kb < num_kb; ++kb) {
+        if (!mbar_wait(&full[s], ph, p.err)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t x_addr = smem_addr(tiles + size_t(s) * C::kStageBytes);
+#pragma unroll
+        for (int kk = 0; kk < kBK / 32; ++kk)
+          umma_i8_ss_pair(d_tmem, sdesc_kmajor_sw128(x_addr + kk * 32),
+                          sdesc_kmajor_sw128(x_addr + C::kHalfBytes + kk * 32), idesc,
+                          (kb | kk) != 0 ? 1u : 0u);
+        const uint32_t e = smem_addr(&empty[s]);
+        umma_commit_pair(e);
+        umma_commit_pair(mapa_shared(e, 1));
+        if (++s == C::kStages) { s = 0; ph ^= 1u; }
+      }
+      if (ok) {
+        const uint32_t f = smem_addr(&acc_full[a]);
+        umma_commit_pair(f);
+        umma_commit_pair(mapa_shared(f, 1));
+      }
+    }
+    // Both accumulators released by both CTAs' epilogues before exit.
+    for (int i = 0; i < 2 && ok; ++i, ++it)
+      if (!mbar_wait(&acc_empty[it & 1], (static_cast<uint32_t>(it >> 1) & 1u) ^ 1u, p.err)) break;
+  } else if (warp >= 4) {
+    const int quarter = warp & 3;
+    int it = 0;
+    for (int tile = pair; tile < num_tiles; tile += n_pairs, ++it) {
+      const int mb = tile / p.tiles_n, nb = tile % p.tiles_n;
+      const int a = it & 1;
+      if (!mbar_wait_warp(&acc_full[a], static_cast<uint32_t>(it >> 1) & 1u, p.err)) break;
+      tc_fence_after();
+      const int64_t row = static_cast<int64_t>(mb) * 256 + rank * 128 + quarter * 32 + lane;
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                             static_cast<uint32_t>(a * 256);
+      const float xs = row < p.m ? __ldg(p.xs + row) : 0.f;
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint32_t acc[32];
+        tmem_ld32(t_row + c * 32, acc);
+        tmem_wait_ld_dep(acc);
+        const int col = nb * 256 + c * 32;
+        if (row < p.m && col < p.n) store32<T>(p, row, col, xs, acc);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_addr(&acc_empty[a]), 0));
+    }
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  __syncwarp();
+  if (warp == 2) tmem_dealloc_pair(tmem_base, C::kTmemCols);
+}
+
+// ------------------------------------------------------------------ narrow
+// One CTA: 128 output channels (M, TMEM lanes) x `cols` rows of x (N, TMEM
+// columns) over its share of k. A cluster (z) shares the tile; each CTA lays
+// its 32-bit sums out in shared memory, [column][lane], and adds up and
+// stores every cluster-size-th group of columns.
+struct Narrow {
+  static constexpr int kWBytes = 128 * kBK;
+  static constexpr int kRing = 96 * 1024;  // two CTAs on an SM
+  static constexpr int kMaxCols = 128;
+  static constexpr int kMaxStages = 5;
+  static constexpr size_t kSmem = 1024 + kRing + 256;
+};
+static_assert(Narrow::kMaxCols * 128 * 4 <= Narrow::kRing, "the sums reuse the ring");
+
+__device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2)
+    gemm_i8_narrow(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                   const __grid_constant__ Params p) {
+  using C = Narrow;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_addr(smem_raw);
+  uint8_t* tiles = smem_raw + ((1024 - (raw_addr & 1023)) & 1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(tiles + C::kRing);
+  uint64_t* empty = full + C::kMaxStages;
+  uint64_t* acc_full = empty + C::kMaxStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+  __shared__ int s_bad;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = static_cast<int>(gridDim.z), part = static_cast<int>(blockIdx.z);
+  const int w_row = static_cast<int>(blockIdx.x) * 128;
+  const int64_t x_row = static_cast<int64_t>(blockIdx.y) * C::kMaxCols;
+  const int stage_bytes = C::kWBytes + p.cols * kBK;
+  const int num_kb = (p.k + kBK - 1) / kBK;
+  const int kb_lo = part * num_kb / split, kb_hi = (part + 1) * num_kb / split;
+  uint32_t tmem_cols = 32;
+  while (static_cast<int>(tmem_cols) < p.cols) tmem_cols *= 2;
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc_full, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmW);
+    s_bad = 0;
+  }
+  if (warp == 2) tmem_alloc(tmem_slot, tmem_cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  if (warp == 0 && lane == 0) {
+    int s = 0;
+    uint32_t ph = 0;
+    for (int kb = kb_lo; kb < kb_hi; ++kb) {
+      if (!mbar_wait(&empty[s], ph ^ 1u, p.err)) break;
+      uint8_t* dst = tiles + s * stage_bytes;
+      mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(stage_bytes));
+      tma_load_2d(&tmW, &full[s], dst, kb * kBK, w_row);
+      tma_load_2d(&tmX, &full[s], dst + C::kWBytes, kb * kBK, static_cast<int>(x_row));
+      if (++s == p.stages) { s = 0; ph ^= 1u; }
+    }
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_s8_s32(128, p.cols);
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int kb = kb_lo; kb < kb_hi; ++kb) {
+      if (!mbar_wait(&full[s], ph, p.err)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t w_addr = smem_addr(tiles + s * stage_bytes);
+#pragma unroll
+      for (int kk = 0; kk < kBK / 32; ++kk)
+        umma_i8_ss(tmem, sdesc_kmajor_sw128(w_addr + kk * 32),
+                   sdesc_kmajor_sw128(w_addr + C::kWBytes + kk * 32), idesc,
+                   (kb > kb_lo || kk > 0) ? 1u : 0u);
+      umma_commit(&empty[s]);
+      if (++s == p.stages) { s = 0; ph ^= 1u; }
+    }
+    if (ok) umma_commit(acc_full);
+    else s_bad = 1;  // the sums are not complete: nothing is stored
+  }
+  // The ring is free once the last MMA has read it: the sums go there.
+  int* sums = reinterpret_cast<int*>(tiles);
+  __syncwarp();
+  if (warp >= 4) {
+    if (mbar_wait_warp(acc_full, 0, p.err)) {
+      tc_fence_after();
+      const int quarter = warp & 3;
+      for (int c = 0; c < p.cols; c += 16) {
+        uint32_t acc[16];
+        tmem_ld16(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(c), acc);
+        tmem_wait_ld_dep16(acc);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          sums[(c + i) * 128 + quarter * 32 + lane] = static_cast<int>(acc[i]);
+      }
+    } else {
+      s_bad = 1;
+    }
+  }
+  tc_fence_before();
+  if (split > 1) cluster_sync();
+  else __syncthreads();
+  tc_fence_after();
+  const int cols = static_cast<int>(min(static_cast<int64_t>(p.cols), p.m - x_row));
+  if (s_bad == 0) {
+    // one warp per column: lane's four channels, one after the other part's sums
+    const int ch = w_row + lane * 4;
+    if (ch < p.n) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(p.ws + ch));
+      for (int c = part * 8 + warp; c < cols; c += split * 8) {
+        const uint32_t at = smem_addr(sums + c * 128 + lane * 4);
+        int4 a = make_int4(0, 0, 0, 0);
+        if (split > 1) {
+          for (int q = 0; q < split; ++q) {
+            const int4 b = ld_cluster_int4(mapa_shared(at, static_cast<uint32_t>(q)));
+            a.x += b.x;
+            a.y += b.y;
+            a.z += b.z;
+            a.w += b.w;
+          }
+        } else {
+          a = *reinterpret_cast<const int4*>(sums + c * 128 + lane * 4);
+        }
+        const float xs = __ldg(p.xs + x_row + c);
+        float4 v = make_float4(static_cast<float>(a.x) * xs * w.x, static_cast<float>(a.y) * xs * w.y,
+                               static_cast<float>(a.z) * xs * w.z, static_cast<float>(a.w) * xs * w.w);
+        const int64_t yi = (x_row + c) * p.n + ch;
+        if constexpr (sizeof(T) == 4) {
+          if (p.residual != nullptr) {
+            const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + yi);
+            v = make_float4(v.x + r.x, v.y + r.y, v.z + r.z, v.w + r.w);
+          }
+          *reinterpret_cast<float4*>(static_cast<float*>(p.y) + yi) = v;
+        } else {
+          if (p.residual != nullptr) {
+            const uint2 u =
+                *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.residual) + yi);
+            const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+            const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+            v = make_float4(v.x + lo.x, v.y + lo.y, v.z + hi.x, v.w + hi.y);
+          }
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + yi) =
+              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        }
+      }
+    }
+  }
+  __syncwarp();
+  if (split > 1) cluster_sync();  // the other parts have read this CTA's sums
+  else __syncthreads();
+  if (warp == 2) tmem_dealloc(tmem, tmem_cols);
+}
+
+template <typename T>
+cudaError_t run_wide(const QuantGemmArgs& g, cudaStream_t st) {
+  CUtensorMap tx, tw;
+  if (!make_tmap_2d_u8(&tx, g.x, g.m, g.k, 128) || !make_tmap_2d_u8(&tw, g.w, g.n, g.k, 128))
+    return cudaErrorInvalidValue;
+  Params p{};
+  p.m = g.m;
+  p.n = g.n;
+  p.k = g.k;
+  p.xs = g.xs;
+  p.ws = g.ws;
+  p.residual = g.residual;
+  p.y = g.y;
+  p.tiles_m = static_cast<int>((g.m + 255) / 256);
+  p.tiles_n = (g.n + 255) / 256;
+  p.err = device_error_word();
+  auto kern = gemm_i8_wide<T>;
+  TG_CUDA_TRY(set_smem_attr_once(reinterpret_cast<const void*>(kern), static_cast<int>(Wide::kSmem)));
+  // Persistent grid: as many pairs as can be resident at once (the SMs of a
+  // pair must share a TPC, so this can be below num_sms() / 2).
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> resident[kMaxDevices];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  int max_pairs = (dev >= 0 && dev < kMaxDevices) ? resident[dev].load() : 0;
+  if (max_pairs <= 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(num_sms() & ~1), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Wide::kSmem;
+    cfg.stream = st;
+    if (cudaOccupancyMaxActiveClusters(&max_pairs, kern, &cfg) != cudaSuccess || max_pairs <= 0) {
+      cudaGetLastError();
+      max_pairs = num_sms() / 2;
+    }
+    if (dev >= 0 && dev < kMaxDevices) resident[dev].store(max_pairs);
+  }
+  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+  const unsigned pairs = static_cast<unsigned>(tiles < max_pairs ? tiles : max_pairs);
+  return launch_pdl(kern, dim3(2 * pairs), dim3(kThreads), Wide::kSmem, st, tx, tw, p);
+}
+
+template <typename T>
+cudaError_t run_narrow(const QuantGemmArgs& g, cudaStream_t st) {
+  using C = Narrow;
+  Params p{};
+  p.m = g.m;
+  p.n = g.n;
+  p.k = g.k;
+  p.xs = g.xs;
+  p.ws = g.ws;
+  p.residual = g.residual;
+  p.y = g.y;
+  p.cols = g.m >= C::kMaxCols ? C::kMaxCols : static_cast<int>((g.m + 15) / 16 * 16);
+  p.stages = C::kRing / (C::kWBytes + p.cols * kBK);
+  if (p.stages > C::kMaxStages) p.stages = C::kMaxStages;
+  p.err = device_error_word();
+  CUtensorMap tx, tw;
+  if (!make_tmap_2d_u8(&tx, g.x, g.m, g.k, p.cols) || !make_tmap_2d_u8(&tw, g.w, g.n, g.k, 128))
+    return cudaErrorInvalidValue;
+  const int tiles_n = (g.n + 127) / 128;
+  const int tiles_m = static_cast<int>((g.m + C::kMaxCols - 1) / C::kMaxCols);
+  // k is split until the CTAs fill the SMs (two fit on one), each keeping two
+  // stages of k at least.
+  const int num_kb = (g.k + kBK - 1) / kBK;
+  int split = 1;
+  while (split < 8 && tiles_n * tiles_m * split * 2 <= 2 * num_sms() && num_kb >= 4 * split) split *= 2;
+  auto kern = gemm_i8_narrow<T>;
+  TG_CUDA_TRY(set_smem_attr_once(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmem)));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles_n), static_cast<unsigned>(tiles_m),
+                     static_cast<unsigned>(split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = static_cast<unsigned>(split);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, tx, tw, p);
+}
+
+}  // namespace
+
+cudaError_t launch_quant_gemm_wide(const QuantGemmArgs& g, cudaStream_t st) {
+  return g.bf16 ? run_wide<__nv_bfloat16>(g, st) : run_wide<float>(g, st);
+}
+
+cudaError_t launch_quant_gemm_narrow(const QuantGemmArgs& g, cudaStream_t st) {
+  return g.bf16 ? run_narrow<__nv_bfloat16>(g, st) : run_narrow<float>(g, st);
+}
+
+}  // namespace tg

@@ -401,12 +401,23 @@ struct QuantGemmArgs {
   bool bf16;                         // type of y and residual (else fp32)
 };
 cudaError_t launch_quant_gemm(const QuantGemmArgs& g, cudaStream_t st);
+// the tensor-core products (k_quant_tc.cu)
+cudaError_t launch_quant_gemm_narrow(const QuantGemmArgs& g, cudaStream_t st);
+cudaError_t launch_quant_gemm_wide(const QuantGemmArgs& g, cudaStream_t st);
 
 // ---- tensor maps (tg_tmap.cu)
 // 2-D bf16 tensor map, row-major [rows, cols] with row stride ld (elements),
 // box [box_rows, 64 cols], 128-byte swizzle. Returns false on failure.
 bool make_tmap_2d_bf16(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld,
                        int box_rows);
+// 2-D map of 8-bit elements, row-major [rows, cols], box [box_rows, 128 cols],
+// 128-byte swizzle.
+bool make_tmap_2d_u8(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows);
+// 4-D bf16 map of a page pool [n_pages][page_size, hkv, dh] (page_stride
+// elements between pages), box {64 columns, 1 head, box_rows, 1 page},
+// 128-byte swizzle; a page index of n_pages reads zeros.
+bool make_tmap_pages_bf16(CUtensorMap* m, const void* base, int dh, int hkv, int page_size,
+                          int64_t n_pages, int64_t page_stride, int box_rows);
 // 2-D bf16 tensor map of 16-column rows (row stride ld elements), box
 // [box_rows, 16], 32-byte swizzle: one MMA K-step per row.
 bool make_tmap_2d_bf16_sw32(CUtensorMap* m, const void* base, int64_t rows, int64_t ld,
