@@ -96,11 +96,11 @@ __global__ void __launch_bounds__(256) quantize_rows(const T* __restrict__ x, in
 
 // ---------------------------------------------------------------- product, few rows
 // y[i, j] = (sum_k xq[i, k] wq[j, k]) xs[i] ws[j] (+ residual). One warp per
-// four output channels and up to eight rows of x: the lanes split k in
+// four output channels and up to four rows of x: the lanes split k in
 // 16-byte pieces, the weights stream from memory once, the rows of x come
 // from the L1 cache. Sums of products of 8-bit integers in 32-bit integers
 // are exact (k <= 131071).
-constexpr int kGvCols = 4, kGvRows = 8;
+constexpr int kGvCols = 4, kGvRows = 4;
 
 __device__ __forceinline__ int dot16(const int4& a, const int4& b, int c) {
   c = __dp4a(a.x, b.x, c);
@@ -171,8 +171,13 @@ cudaError_t launch_quantize_rows(const void* x, int64_t x_stride, int64_t rows, 
 
 cudaError_t launch_quant_gemm(const QuantGemmArgs& g, cudaStream_t st) {
   if (g.m <= 0) return cudaSuccess;
-  if (g.m > 256) return launch_quant_gemm_wide(g, st);
-  if (g.m > 4) return launch_quant_gemm_narrow(g, st);
+  // Up to four rows the warps' dot products need no tensor core (1 x 4096 x
+  // 2048: 3.9 us, narrow 4.9). Above, the narrow tiles until the wide ones
+  // come near to a wave of CTA pairs (200 x 4096 x 2048, 16 wide tiles: narrow
+  // 10.2 us, wide 14.2; 1024 x 4096 x 2048, 64: 14.7 and 14.6; 512 x 12288 x
+  // 2048, 96: 26.1 and 21.3).
+  const int64_t wide_tiles = (g.m + 255) / 256 * ((g.n + 255) / 256);
+  if (g.m > 4) return wide_tiles < 64 ? launch_quant_gemm_narrow(g, st) : launch_quant_gemm_wide(g, st);
   const dim3 grid(static_cast<unsigned>((g.n + 8 * kGvCols - 1) / (8 * kGvCols)),
                   static_cast<unsigned>((g.m + kGvRows - 1) / kGvRows));
   if (g.bf16) TG_CUDA_TRY(launch_pdl(quant_gemv<__nv_bfloat16>, grid, dim3(256), 0, st, g));

@@ -80,68 +80,112 @@ struct Wide {
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kStages = 6;
   static constexpr int kTmemCols = 512;
-  static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + 256;
+  static constexpr int kOffOut = kStages * kStageBytes;  // two 4 KB buffers an epilogue warp
+  static constexpr int kOffBar = kOffOut + 4 * 2 * 4096;
+  static constexpr size_t kSmem = 1024 + kOffBar + 256;
 };
 
-// 32 accumulators of one row, scaled (and added to the residual), to y.
+// One warp's 32 rows x 128 bytes of outputs (64 bf16 or 32 fp32 columns from
+// column `col` on): the accumulators, scaled, plus the residual, into `buf`
+// (rows of 128 bytes, 16-byte unit u of row r at u ^ (r & 7), the layout of
+// the output map's boxes) and from there by TMA. A thread's own row is a
+// piece of 128 bytes far from its neighbour's: stored and read directly it
+// costs a sector per thread and instruction, which made the epilogue the
+// longer side of a tile at k = 2048 (8192 x 12288: 180 us).
 template <typename T>
-__device__ __forceinline__ void store32(const Params& p, int64_t row, int col, float xs,
-                                        const uint32_t (&acc)[32]) {
-  float v[32];
+__device__ __forceinline__ void scale_store(const Params& p, const CUtensorMap* tmY, int64_t row0,
+                                            int col, float xs, uint32_t t_col, uint8_t* buf) {
+  constexpr int kVec = 16 / static_cast<int>(sizeof(T));  // outputs of a 16-byte unit
+  constexpr int kCols = 8 * kVec;
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  // the residual, 4 rows of 128 bytes an instruction
+  const bool res = p.residual != nullptr;
+  const int u = lane & 7;
+  const int64_t c0 = col + u * kVec;
+  if (res) {
+    uint4 t[8];
 #pragma unroll
-  for (int j = 0; j < 32; j += 4) {
-    const float4 w = __ldg(reinterpret_cast<const float4*>(p.ws + col + j));
-    v[j] = static_cast<float>(static_cast<int>(acc[j])) * xs * w.x;
-    v[j + 1] = static_cast<float>(static_cast<int>(acc[j + 1])) * xs * w.y;
-    v[j + 2] = static_cast<float>(static_cast<int>(acc[j + 2])) * xs * w.z;
-    v[j + 3] = static_cast<float>(static_cast<int>(acc[j + 3])) * xs * w.w;
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = row0 + 4 * i + (lane >> 3);
+      t[i] = make_uint4(0, 0, 0, 0);
+      if (r < p.m && c0 < p.n)
+        t[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.residual) + r * p.n + c0);
+    }
+    if (lane == 0) bulk_wait_read_but_one();  // the store that last used buf has read it
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      *reinterpret_cast<uint4*>(buf + r * 128 + ((u ^ (r & 7)) << 4)) = t[i];
+    }
+  } else if (lane == 0) {
+    bulk_wait_read_but_one();
   }
-  const int64_t at = row * p.n + col;
-  if constexpr (sizeof(T) == 4) {
-    const float4* r = reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + at);
-    float4* y = reinterpret_cast<float4*>(static_cast<float*>(p.y) + at);
+  __syncwarp();
+  uint8_t* mine = buf + lane * 128;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float4 o = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-      if (p.residual != nullptr) {
-        const float4 t = r[j];
-        o.x += t.x;
-        o.y += t.y;
-        o.z += t.z;
-        o.w += t.w;
-      }
-      y[j] = o;
+  for (int h = 0; h < kCols / 32; ++h) {
+    uint32_t acc[32];
+    tmem_ld32(t_col + h * 32, acc);
+    tmem_wait_ld_dep(acc);
+    const int hc = col + h * 32;
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const float4 w = hc < p.n ? __ldg(reinterpret_cast<const float4*>(p.ws + hc + j))
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[j] = static_cast<float>(static_cast<int>(acc[j])) * xs * w.x;
+      v[j + 1] = static_cast<float>(static_cast<int>(acc[j + 1])) * xs * w.y;
+      v[j + 2] = static_cast<float>(static_cast<int>(acc[j + 2])) * xs * w.z;
+      v[j + 3] = static_cast<float>(static_cast<int>(acc[j + 3])) * xs * w.w;
     }
-  } else {
-    const uint4* r = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + at);
-    uint4* y = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + at);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (p.residual != nullptr) {
-        const uint4 t = r[j];
-        const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&t);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = __bfloat1622float2(e[i]);
-          v[8 * j + 2 * i] += f.x;
-          v[8 * j + 2 * i + 1] += f.y;
+    for (int q = 0; q < 32 / kVec; ++q) {
+      uint4* at = reinterpret_cast<uint4*>(mine + (((h * 32 / kVec + q) ^ (lane & 7)) << 4));
+      if constexpr (sizeof(T) == 4) {
+        if (res) {
+          const uint4 r = *at;
+          v[4 * q] += __uint_as_float(r.x);
+          v[4 * q + 1] += __uint_as_float(r.y);
+          v[4 * q + 2] += __uint_as_float(r.z);
+          v[4 * q + 3] += __uint_as_float(r.w);
         }
+        *at = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                         __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+      } else {
+        if (res) {
+          const uint4 r = *at;
+          const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&r);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = __bfloat1622float2(e[i]);
+            v[8 * q + 2 * i] += f.x;
+            v[8 * q + 2 * i + 1] += f.y;
+          }
+        }
+        *at = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                         pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
+                         pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
       }
-      y[j] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                        pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
     }
+  }
+  fence_async_smem();
+  __syncwarp();
+  if (lane == 0) {  // rows past m and columns past n are not written
+    if (row0 < p.m && col < p.n) tma_store_2d(tmY, buf, col, static_cast<int>(row0));
+    bulk_commit();
   }
 }
 
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_i8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                 const __grid_constant__ Params p) {
+                 const __grid_constant__ CUtensorMap tmY, const __grid_constant__ Params p) {
   using C = Wide;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_addr(smem_raw);
   uint8_t* tiles = smem_raw + ((1024 - (raw_addr & 1023)) & 1023);
-  uint64_t* full = reinterpret_cast<uint64_t*>(tiles + size_t(C::kStages) * C::kStageBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(tiles + C::kOffBar);
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;
   uint64_t* acc_empty = acc_full + 2;
@@ -232,28 +276,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!mbar_wait(&acc_empty[it & 1], (static_cast<uint32_t>(it >> 1) & 1u) ^ 1u, p.err)) break;
   } else if (warp >= 4) {
     const int quarter = warp & 3;
+    uint8_t* out = tiles + C::kOffOut + quarter * 8192;
+    int flip = 0;
     int it = 0;
     for (int tile = pair; tile < num_tiles; tile += n_pairs, ++it) {
       const int mb = tile / p.tiles_n, nb = tile % p.tiles_n;
       const int a = it & 1;
       if (!mbar_wait_warp(&acc_full[a], static_cast<uint32_t>(it >> 1) & 1u, p.err)) break;
       tc_fence_after();
-      const int64_t row = static_cast<int64_t>(mb) * 256 + rank * 128 + quarter * 32 + lane;
+      const int64_t row0 = static_cast<int64_t>(mb) * 256 + rank * 128 + quarter * 32;
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                              static_cast<uint32_t>(a * 256);
-      const float xs = row < p.m ? __ldg(p.xs + row) : 0.f;
+      const float xs = row0 + lane < p.m ? __ldg(p.xs + row0 + lane) : 0.f;
+      constexpr int kStep = 128 / static_cast<int>(sizeof(T));
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        uint32_t acc[32];
-        tmem_ld32(t_row + c * 32, acc);
-        tmem_wait_ld_dep(acc);
-        const int col = nb * 256 + c * 32;
-        if (row < p.m && col < p.n) store32<T>(p, row, col, xs, acc);
+      for (int c = 0; c < 256; c += kStep) {
+        scale_store<T>(p, &tmY, row0, nb * 256 + c, xs, t_row + c, out + (flip ? 4096 : 0));
+        flip ^= 1;
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_addr(&acc_empty[a]), 0));
     }
+    if (lane == 0) bulk_wait_read_all();  // the buffers are read before the CTA may exit
   }
   tc_fence_before();
   cluster_sync();
@@ -431,8 +476,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 template <typename T>
 cudaError_t run_wide(const QuantGemmArgs& g, cudaStream_t st) {
-  CUtensorMap tx, tw;
-  if (!make_tmap_2d_u8(&tx, g.x, g.m, g.k, 128) || !make_tmap_2d_u8(&tw, g.w, g.n, g.k, 128))
+  CUtensorMap tx, tw, ty;
+  if (!make_tmap_2d_u8(&tx, g.x, g.m, g.k, 128) || !make_tmap_2d_u8(&tw, g.w, g.n, g.k, 128) ||
+      !make_tmap_2d_out(&ty, g.y, g.m, g.n, g.bf16, 32))
     return cudaErrorInvalidValue;
   Params p{};
   p.m = g.m;
@@ -468,7 +514,7 @@ cudaError_t run_wide(const QuantGemmArgs& g, cudaStream_t st) {
   }
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   const unsigned pairs = static_cast<unsigned>(tiles < max_pairs ? tiles : max_pairs);
-  return launch_pdl(kern, dim3(2 * pairs), dim3(kThreads), Wide::kSmem, st, tx, tw, p);
+  return launch_pdl(kern, dim3(2 * pairs), dim3(kThreads), Wide::kSmem, st, tx, tw, ty, p);
 }
 
 template <typename T>

@@ -413,6 +413,10 @@ bool make_tmap_2d_bf16(CUtensorMap* m, const void* base, int64_t rows, int64_t c
 // 2-D map of 8-bit elements, row-major [rows, cols], box [box_rows, 128 cols],
 // 128-byte swizzle.
 bool make_tmap_2d_u8(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows);
+// 2-D map of a contiguous bf16 or fp32 matrix [rows, cols] written by TMA
+// stores: box [box_rows, 128 bytes of a row], 128-byte swizzle.
+bool make_tmap_2d_out(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, bool bf16,
+                      int box_rows);
 // 4-D bf16 map of a page pool [n_pages][page_size, hkv, dh] (page_stride
 // elements between pages), box {64 columns, 1 head, box_rows, 1 page},
 // 128-byte swizzle; a page index of n_pages reads zeros.

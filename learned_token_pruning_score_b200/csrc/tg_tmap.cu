@@ -54,6 +54,21 @@ bool make_tmap_2d_u8(CUtensorMap* m, const void* base, int64_t rows, int64_t col
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tmap_2d_out(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, bool bf16,
+                      int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t e = bf16 ? 2 : 4;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * e};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / e), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1u, 1u};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_tmap_pages_bf16(CUtensorMap* m, const void* base, int dh, int hkv, int page_size,
                           int64_t n_pages, int64_t page_stride, int box_rows) {
   auto fn = encode_fn();
