@@ -711,11 +711,12 @@ typedef enum {
   TG_K_GDN_RECUR = 22,       /* Gated DeltaNet: the state across the chunks          */
   TG_K_GDN_OUT = 23,         /* Gated DeltaNet: gated output RMSNorm                 */
   TG_K_FOLD_NORM = 24,       /* tg_fold_norm_weight                                  */
-  TG_K_PAGED_APPEND = 25,    /* tg_paged_append                                      */
-  TG_K_PAGED_ATTN = 26,      /* tg_paged_attn                                        */
-  TG_K_QUANTIZE = 27,        /* tg_quantize_rows                                     */
-  TG_K_GEMM_INT = 28,        /* tg_linear_quantized                                  */
-  TG_K_COUNT = 29
+  /* 25 is not assigned */
+  TG_K_PAGED_APPEND = 26,    /* tg_paged_append                                      */
+  TG_K_PAGED_ATTN = 27,      /* tg_paged_attn                                        */
+  TG_K_QUANTIZE = 28,        /* tg_quantize_rows                                     */
+  TG_K_GEMM_INT = 29,        /* tg_linear_quantized                                  */
+  TG_K_COUNT = 30
 } tg_kernel;
 
 typedef struct {

@@ -328,8 +328,9 @@ __global__ void __launch_bounds__(kSimtThreads)
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        const bool seen = kv0 + tx + 8 * i < limit[r] && !(s[r][i] == -INFINITY);
         const float w = exp2f(s[r][i] - m_use);
-        sm.p[2 * ty + r][tx + 8 * i] = w;
+        sm.p[2 * ty + r][tx + 8 * i] = seen ? w : -1.0f;
         sum += w;
       }
 #pragma unroll
@@ -345,13 +346,12 @@ __global__ void __launch_bounds__(kSimtThreads)
       }
     }
     __syncwarp();  // a row's weights are written and read by one warp
-    // keys that only some rows see are skipped by the others (not weighted
-    // with zero: a value that a row must not see may be infinite or NaN)
-    const bool some = kv0 + kSimtKeys > limit[0] || kv0 + kSimtKeys > limit[1];
+    // keys that a row does not see (weight -1) are skipped, not weighted with
+    // zero: their values may be infinite or NaN
 #pragma unroll 2
     for (int j = 0; j < kSimtKeys; ++j) {
       const float p0 = sm.p[2 * ty][j], p1 = sm.p[2 * ty + 1][j];
-      const bool see0 = !some || kv0 + j < limit[0], see1 = !some || kv0 + j < limit[1];
+      const bool see0 = !(p0 < 0.f), see1 = !(p1 < 0.f);
 #pragma unroll
       for (int c = 0; c < kCols; ++c) {
         const float4 vv = *reinterpret_cast<const float4*>(&sm.v[j][4 * tx + 32 * c]);
@@ -428,10 +428,7 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, bool bf16, cudaStream_
   return a.kv.dh == 128 ? run_append<float, 128>(a, st) : run_append<float, 64>(a, st);
 }
 
-cudaError_t launch_paged_attn_simt(const PagedAttnArgs& a, bool bf16, cudaStream_t st) {
-  if (a.rows <= 0 || a.batch <= 0) return cudaSuccess;
-  if (bf16)
-    return a.kv.dh == 128 ? run_simt<__nv_bfloat16, 128>(a, st) : run_simt<__nv_bfloat16, 64>(a, st);
+cudaError_t launch_paged_attn_simt(const PagedAttnArgs& a, cudaStream_t st) {
   return a.kv.dh == 128 ? run_simt<float, 128>(a, st) : run_simt<float, 64>(a, st);
 }
 

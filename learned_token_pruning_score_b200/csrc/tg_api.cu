@@ -974,7 +974,10 @@ size_t tg_workspace_size(tg_op op, const tg_shape* s) {
       return DecodePlan(nullptr, m, s->k).bytes;
     }
     case TG_OP_PAGED_ATTN:
-      return 0;
+      if (s->dtype != TG_BF16 || s->k < 1 || s->n < 1 || s->n_heads_kv < 1 || s->head_dim < 1 ||
+          s->n_heads_q < s->n_heads_kv)
+        return 0;
+      return paged_attn_ws_bytes(s->k, s->n, s->n_heads_q, s->n_heads_kv, s->head_dim);
   }
   return 0;
 }
@@ -1950,6 +1953,14 @@ tg_status paged_view(const tg_paged_kv* c, const int32_t* cu_q, const int32_t* k
 }
 }  // namespace
 
+namespace tg {
+size_t paged_attn_ws_bytes(int64_t rows, int64_t batch, int hq, int hkv, int dh) {
+  // one split writes the output itself
+  const size_t s = paged_max_splits(rows, batch, hq, hkv, 16);
+  return s > 1 ? align_up(s * size_t(rows) * size_t(hq) * size_t(dh + 2) * 4, 256) : 256;
+}
+}  // namespace tg
+
 extern "C" {
 
 tg_status tg_paged_append(const tg_paged_kv* cache, const void* q, int64_t q_stride, const void* k,
@@ -2037,12 +2048,15 @@ tg_status tg_paged_attn(const tg_paged_kv* cache, const void* q, int64_t q_strid
   a.out = out;
   a.lse = lse;
   a.err = device_error_word();
-  (void)ws;
-  (void)ws_bytes;
+  if (dt == TG_BF16) {
+    TG_CHECK(ws != nullptr && ws_bytes >= paged_attn_ws_bytes(rows, batch, hq, hkv, dh),
+             TG_ERR_WORKSPACE);
+    TG_CHECK(aligned16(ws), TG_ERR_INVALID_ARG);
+  }
   const double bytes = 2.0 * rows * hq * dh * double(elem_size(dt));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return cuda_status(traced(TG_K_PAGED_ATTN, rows, 0.0, bytes, st, [&] {
-    return launch_paged_attn_simt(a, dt == TG_BF16, st);
+    return dt == TG_BF16 ? launch_paged_decode(a, ws, st) : launch_paged_attn_simt(a, st);
   }));
 }
 
@@ -2084,7 +2098,7 @@ const char* tg_kernel_name(int32_t kernel) {
       "rope_prep", "attention_tc", "select", "compact", "gemm_f32", "attention_f32", "f32_helper",
       "gemm_tc_qkv", "rope_table", "decode_step", "attn_bwd_prep", "attn_bwd_dkdv",
       "attn_bwd_dq", "attn_bwd_final", "gdn_prep", "gdn_chunk", "gdn_recur", "gdn_out",
-      "fold_norm", "paged_append", "paged_attn", "quantize", "gemm_int"};
+      "fold_norm", "unknown", "paged_append", "paged_attn", "quantize", "gemm_int"};
   return (kernel >= 0 && kernel < TG_K_COUNT) ? names[kernel] : "unknown";
 }
 

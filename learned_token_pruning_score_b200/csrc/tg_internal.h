@@ -384,9 +384,37 @@ struct PagedAttnArgs {
   void* out;                        // [rows, hq, dh]
   float* lse;                       // [hq, rows] or null
   unsigned int* err;
+  // split keys (bf16): split s covers keys [s chunk, (s + 1) chunk)
+  int splits;
+  int64_t chunk;
+  float* part_o;                    // [splits][rows][hq][dh], unnormalised
+  float* part_ml;                   // [splits][rows][hq][2]: maximum (log2 units) and sum
 };
-// CUDA cores, fp32 arithmetic
-cudaError_t launch_paged_attn_simt(const PagedAttnArgs& a, bool bf16, cudaStream_t st);
+// Upper bound of the row tiles of a call: rows are (token, head of the group)
+// pairs and each request's last tile may be short.
+inline int64_t paged_row_tiles(int64_t rows, int64_t batch, int hq, int hkv, int tile) {
+  return rows * (hq / hkv) / tile + (batch < rows ? batch : rows);
+}
+// Most splits of a call: up to 64, while the (row tile, KV head, split) jobs
+// stay within 64 for each of 148 SMs, which also bounds the partial results
+// (of at most `tile` rows a job) whatever the batch.
+inline int paged_max_splits(int64_t rows, int64_t batch, int hq, int hkv, int tile) {
+  const int64_t jobs = paged_row_tiles(rows, batch, hq, hkv, tile) * hkv;
+  const int64_t s = 64 * 148 / (jobs > 0 ? jobs : 1);
+  return static_cast<int>(s < 1 ? 1 : s > 64 ? 64 : s);
+}
+size_t paged_attn_ws_bytes(int64_t rows, int64_t batch, int hq, int hkv, int dh);
+// Lays the partial results of a->splits splits out in the workspace.
+inline void paged_partials(PagedAttnArgs* a, void* ws) {
+  const size_t n = static_cast<size_t>(a->splits) * a->rows * a->hq;
+  a->part_o = static_cast<float*>(ws);
+  a->part_ml = a->part_o + n * a->kv.dh;
+}
+// fp32, CUDA cores (k_paged.cu)
+cudaError_t launch_paged_attn_simt(const PagedAttnArgs& a, cudaStream_t st);
+// bf16: few rows a request (k_paged_decode.cu)
+cudaError_t launch_paged_decode(PagedAttnArgs a, void* ws, cudaStream_t st);
+cudaError_t launch_paged_merge(const PagedAttnArgs& a, cudaStream_t st);
 
 // ---- 8-bit integers (k_quant.cu)
 // xq = rint(127 x / amax), scale = amax / 127 per row; cols % 16 == 0.

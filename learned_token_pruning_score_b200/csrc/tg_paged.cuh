@@ -15,6 +15,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // zero and not NaN; times any gain above 1e-8 it lands below this bound.
 constexpr float kMaskedLogit = -1e30f;
 constexpr float kLowestBias = -1e38f;
+// Only keys with a bias below this one can be removed by it (gains up to
+// 1e10): the kernels look at a block's logits one by one when it holds some.
+constexpr float kRemovableBias = -1e20f;
 
 __device__ __forceinline__ float key_bias(float b) { return b < kLowestBias ? kLowestBias : b; }
 
