@@ -606,7 +606,9 @@ tg_status tg_paged_append(const tg_paged_kv* cache, const void* q, int64_t q_str
  * -inf, removes the key; a row that has no key left (or kv_len[b] < n_b)
  * gets zeros and lse -inf. Values of keys that a row does not see never reach
  * it, whatever they hold. The chunk's own rows must be in the cache
- * (tg_paged_append). Workspace: tg_workspace_size(TG_OP_PAGED_ATTN) with
+ * (tg_paged_append). rows x hq < 2^31 and max_kv <= 2^30 (else
+ * TG_ERR_UNSUPPORTED).
+ * Workspace: tg_workspace_size(TG_OP_PAGED_ATTN) with
  * n = batch, k = rows, the heads, head_dim and dtype; it carries nothing from
  * call to call. bf16 (products of bf16 values on the tensor cores, sums and
  * softmax in fp32) or fp32 (CUDA cores).

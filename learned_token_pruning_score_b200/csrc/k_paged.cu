@@ -92,11 +92,11 @@ __global__ void __launch_bounds__(kAppThreads) paged_append(const __grid_constan
     if (b < a.batch) {  // rows behind the last request are left alone
       const int64_t lo = __ldg(a.cu_q + b), hi = __ldg(a.cu_q + b + 1);
       const int64_t dst = static_cast<int64_t>(__ldg(a.kv_len + b)) - (hi - lo) + (t - lo);
-      const int64_t blk = dst / a.kv.page_size;
+      const int64_t blk = dst >> a.kv.page_shift;
       bad = lo > t || dst < 0 || blk >= a.kv.table_stride;
       if (!bad) {
         page = __ldg(a.kv.table + static_cast<int64_t>(b) * a.kv.table_stride + blk);
-        row = static_cast<int>(dst % a.kv.page_size);
+        row = static_cast<int>(dst) & (a.kv.page_size - 1);
         bad = page < 0 || page >= a.kv.n_pages;
       }
     }
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kSimtThreads)
   const int group = a.hq / a.kv.hkv;
   const int g = blockIdx.y;
   if (threadIdx.x < 32) {
-    const PagedTile t = find_tile(a, kSimtRows, blockIdx.x);
+    const PagedTile t = find_tile(a, kSimtRows, static_cast<int>(blockIdx.x));
     if (threadIdx.x == 0) s_tile = t;
   }
   __syncthreads();
@@ -235,15 +235,15 @@ __global__ void __launch_bounds__(kSimtThreads)
   if (tile.req < 0) return;
   const int tid = threadIdx.x, tx = tid & 7, ty = tid >> 3;
   // rows of the tile: token (row0 + r) / group of the request, head (row0 + r) % group
-  const int n_rows = static_cast<int>(min(static_cast<int64_t>(kSimtRows), tile.n * group - tile.row0));
+  const int n_rows = min(kSimtRows, tile.n * group - tile.row0);
   for (int e = tid; e < kSimtRows * (kDh / kVec); e += kSimtThreads) {
     const int r = e / (kDh / kVec), c = (e % (kDh / kVec)) * kVec;
     float f[kVec];
     uint4 u = make_uint4(0, 0, 0, 0);
     if (r < n_rows) {
-      const int64_t rr = tile.row0 + r;
+      const int rr = tile.row0 + r;
       u = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
-                                          (tile.tok0 + rr / group) * a.q_stride +
+                                          static_cast<int64_t>(tile.tok0 + rr / group) * a.q_stride +
                                           (g * group + rr % group) * kDh + c);
     }
     unpack(u, f);
@@ -251,17 +251,17 @@ __global__ void __launch_bounds__(kSimtThreads)
     for (int i = 0; i < kVec; ++i) sm.q[r][c + i] = f[i];
   }
   float scale[2], gain[2];
-  int64_t limit[2];  // keys that the row sees
+  int limit[2];  // keys that the row sees
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = 2 * ty + i;
-    const int64_t rr = tile.row0 + r;
-    const int h = g * group + static_cast<int>(rr % group);
+    const int rr = tile.row0 + r;
+    const int h = g * group + rr % group;
     scale[i] = kLog2e / (sqrtf(static_cast<float>(kDh)) * (a.tau ? __ldg(a.tau + h) : 1.0f));
     gain[i] = a.gain && a.kv.bias ? __ldg(a.gain + h) * kLog2e : 0.0f;
     limit[i] = r < n_rows ? tile.past + rr / group + 1 : 0;
   }
-  const int64_t kv_end = tile.past + (tile.row0 + n_rows - 1) / group + 1;  // last row's limit
+  const int kv_end = tile.past + (tile.row0 + n_rows - 1) / group + 1;  // last row's limit
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   float4 o[2][kCols];
 #pragma unroll
@@ -269,24 +269,24 @@ __global__ void __launch_bounds__(kSimtThreads)
 #pragma unroll
     for (int c = 0; c < kCols; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
 
-  for (int64_t kv0 = 0; kv0 < kv_end; kv0 += kSimtKeys) {
+  for (int kv0 = 0; kv0 < kv_end; kv0 += kSimtKeys) {
     __syncthreads();  // the last tile's keys are read
     for (int e = tid; e < kSimtKeys * (kDh / kVec); e += kSimtThreads) {
       const int r = e / (kDh / kVec), c = (e % (kDh / kVec)) * kVec;
-      const int64_t j = kv0 + r;
+      const int j = kv0 + r;
       float fk[kVec], fv[kVec];
       uint4 uk = make_uint4(0, 0, 0, 0), uv = uk;
       float b = 0.f;
       if (j < kv_end) {
         const int64_t page = page_of(a, tile.req, j);
         if (page >= 0) {
-          const int64_t off = ((j % a.kv.page_size) * a.kv.hkv + g) * kDh + c;
+          const int64_t off = (static_cast<int64_t>(row_in_page(a, j)) * a.kv.hkv + g) * kDh + c;
           uk = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.kv.k) +
                                                page * a.kv.k_page_stride + off);
           uv = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.kv.v) +
                                                page * a.kv.v_page_stride + off);
           if (c == 0 && a.kv.bias)
-            b = key_bias(a.kv.bias[page * a.kv.bias_page_stride + j % a.kv.page_size]);
+            b = key_bias(a.kv.bias[page * a.kv.bias_page_stride + row_in_page(a, j)]);
         }
       }
       unpack(uk, fk);
@@ -373,9 +373,9 @@ __global__ void __launch_bounds__(kSimtThreads)
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     if (2 * ty + r >= n_rows) continue;
-    const int64_t rr = tile.row0 + 2 * ty + r;
+    const int rr = tile.row0 + 2 * ty + r;
     const int64_t t = tile.tok0 + rr / group;
-    const int h = g * group + static_cast<int>(rr % group);
+    const int h = g * group + rr % group;
     const bool any = l[r] != 0.f;  // a row that sees nothing is zero
     const float inv = any ? 1.0f / l[r] : 0.f;
     if (a.lse != nullptr && tx == 0)
@@ -408,9 +408,7 @@ cudaError_t run_append(const PagedAppendArgs& a, cudaStream_t st) {
 
 template <typename T, int kDh>
 cudaError_t run_simt(const PagedAttnArgs& a, cudaStream_t st) {
-  const int group = a.hq / a.kv.hkv;
-  // an upper bound of the row tiles: each request's last one may be short
-  const int64_t tiles = a.rows * group / kSimtRows + (a.batch < a.rows ? a.batch : a.rows);
+  const int64_t tiles = paged_row_tiles(a.rows, a.batch, a.hq, a.kv.hkv, kSimtRows);
   constexpr int kBytes = static_cast<int>(sizeof(SimtSmem<T, kDh>));
   auto kern = paged_attn_simt<T, kDh>;
   TG_CUDA_TRY(set_smem_attr_once(reinterpret_cast<const void*>(kern), kBytes));

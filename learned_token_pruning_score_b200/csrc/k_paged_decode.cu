@@ -63,14 +63,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void tma_load_4d(const CUtensorMap* m, uint64_t* bar, void* dst, int x, int y,
-                                            int z, int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_addr(dst)),
-      "l"(m), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
-      : "memory");
-}
 
 // Clears the halves of a bf16 pair whose key no row sees; where only some
 // rows see it (bit of `partial`), clears an infinity or NaN too and notes it.
@@ -89,13 +81,6 @@ __device__ __forceinline__ uint32_t clean_pair(uint32_t v, uint32_t dead, uint32
   return v;
 }
 
-// Weight of a partial state (maximum m, sum l) under the maximum `top` of all.
-// A state without keys (l = 0) has none; one whose logits are all NaN has m =
-// -inf and l = NaN, and passes that on.
-__device__ __forceinline__ float state_weight(float m, float l, float top) {
-  return l == 0.f ? 0.f : ex2_approx(m - (top == -INFINITY ? 0.f : top));
-}
-
 template <int kDh>
 __global__ void __launch_bounds__(kThreads, 2)
     paged_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -110,14 +95,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ int s_found;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.kv.hkv));
-  const int64_t rest = blockIdx.x / static_cast<unsigned>(a.kv.hkv);
-  const int split = static_cast<int>(rest % a.splits);
-  const int64_t tile_idx = rest / a.splits;
+  const int rest = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.kv.hkv));
+  const int split = rest % a.splits, tile_idx = rest / a.splits;
   const int group = a.hq / a.kv.hkv;
   pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);  // the fetch (and its bytes), the biases
       mbar_init(&empty[s], 4);
     }
     fence_mbar_init();
@@ -133,17 +117,18 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   const PagedTile tile = s_tile;
   if (tile.req < 0) return;
-  const int n_rows = static_cast<int>(min(static_cast<int64_t>(kRows), tile.n * group - tile.row0));
+  const int n_rows = min(kRows, tile.n * group - tile.row0);
   // keys that the first and the last row of the tile see
-  const int64_t min_limit = tile.past + tile.row0 / group + 1;
-  const int64_t max_limit = tile.past + (tile.row0 + n_rows - 1) / group + 1;
-  const int64_t lo = split * a.chunk;
-  const int64_t hi = min(max_limit, lo + a.chunk);
-  const int blocks = hi > lo ? static_cast<int>((hi - lo + kKeys - 1) / kKeys) : 0;
+  const int min_limit = tile.past + tile.row0 / group + 1;
+  const int max_limit = tile.past + (tile.row0 + n_rows - 1) / group + 1;
+  const int64_t lo64 = split * a.chunk;
+  const int hi = static_cast<int>(min(static_cast<int64_t>(max_limit), lo64 + a.chunk));
+  const int blocks = hi > lo64 ? static_cast<int>((hi - lo64 + kKeys - 1) / kKeys) : 0;
+  const int lo = static_cast<int>(lo64);  // (not used when behind every key)
 
   float o[kDh / 8][4];
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  const int64_t row[2] = {tile.row0 + (lane >> 2), tile.row0 + (lane >> 2) + 8};
+  const int row[2] = {tile.row0 + (lane >> 2), tile.row0 + (lane >> 2) + 8};
   float gain2[2];
 
   if (warp == 4) {
@@ -153,59 +138,87 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int n_box = kKeys / box;             // boxes of a block (a power of two)
     const int n_load = n_box * 2 * C::kSubs;   // loads of a block: box, K or V, columns
     const int my_box = lane & (n_box - 1), my_part = lane / n_box;
-    // page of this lane's box of block i (n_pages, read as zeros, where the
-    // table is out of range), -1 behind the split's keys
-    auto page_at = [&](int i) -> int {
-      const int64_t j = lo + static_cast<int64_t>(i) * kKeys + my_box * box;
-      if (i >= blocks || j >= hi) return -1;
+    // The split's pages, 32 boxes (a group) a load: lane l holds box 32 grp + l
+    // (n_pages, read as zeros, where the table is out of range; -1 behind the
+    // keys). Two groups are held, so that no fetch waits for the table.
+    auto load_group = [&](int grp) -> int {
+      const int64_t j64 = lo64 + (static_cast<int64_t>(grp) * 32 + lane) * box;
+      if (j64 >= hi) return -1;
+      const int j = static_cast<int>(j64);
       const int64_t p = page_of(a, tile.req, j);
       return p < 0 ? static_cast<int>(a.kv.n_pages) : static_cast<int>(p);
     };
-    auto bias_at = [&](int i, int pg, int key) -> float {
-      const int owner = __shfl_sync(0xFFFFFFFFu, pg, key / box);
-      if (a.kv.bias == nullptr || owner < 0 || owner >= a.kv.n_pages) return 0.f;
-      const int64_t j = lo + static_cast<int64_t>(i) * kKeys + key;
-      return key_bias(__ldg(a.kv.bias + owner * a.kv.bias_page_stride + j % page));
+    int grp0 = 0, cur = load_group(0), nxt = load_group(1);
+    auto page_at = [&](int i, int b) -> int {
+      const int idx = i * n_box + b;
+      const int p0 = __shfl_sync(0xFFFFFFFFu, cur, idx & 31), p1 = __shfl_sync(0xFFFFFFFFu, nxt, idx & 31);
+      return (idx >> 5) == grp0 ? p0 : p1;
     };
-    int pg = page_at(0), pg1 = page_at(1);
-    float b0 = bias_at(0, pg, lane), b1 = bias_at(0, pg, lane + 32);
-    for (int i = 0; i < blocks; ++i) {
-      const int s = i % C::kStages;
-      const int pg2 = page_at(i + 2);
-      const float nb0 = bias_at(i + 1, pg1, lane), nb1 = bias_at(i + 1, pg1, lane + 32);
-      if (!mbar_wait_warp(&empty[s], ((i / C::kStages) & 1) ^ 1, a.err)) break;
-      s_bias[s][lane] = b0;
-      s_bias[s][lane + 32] = b1;
-      const int n_live = __popc(__ballot_sync(0xFFFFFFFFu, pg >= 0 && lane < n_load));
-      __syncwarp();
+    auto bias_at = [&](int i, int key) -> float {
+      const int64_t p = page_at(i, key / box);
+      if (a.kv.bias == nullptr || p < 0 || p >= a.kv.n_pages) return 0.f;
+      const int j = lo + i * kKeys + key;
+      return key_bias(__ldg(a.kv.bias + p * a.kv.bias_page_stride + row_in_page(a, j)));
+    };
+    auto fetch = [&](int i, int s) {
+      const int pg = page_at(i, my_box);
+      const bool go = pg >= 0 && lane < n_load;
+      const int n_live = __popc(__ballot_sync(0xFFFFFFFFu, go));
       if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(n_live * box * 128));
       __syncwarp();
-      if (pg >= 0 && lane < n_load) {
+      if (go) {
         const int sub = my_part % C::kSubs, is_v = my_part / C::kSubs;
-        const int64_t j = lo + static_cast<int64_t>(i) * kKeys + my_box * box;
+        const int j = lo + i * kKeys + my_box * box;
         tma_load_4d(is_v ? &tmV : &tmK, &full[s],
                     ring + s * C::kStageBytes + (is_v * C::kSubs + sub) * C::kSub + my_box * box * 128,
-                    sub * 64, g, static_cast<int>(j % page), pg);
+                    sub * 64, g, row_in_page(a, j), pg);
       }
-      pg = pg1;
-      pg1 = pg2;
-      b0 = nb0;
-      b1 = nb1;
+    };
+    // the ring's first fill at once; then, a block at a time, its biases (read
+    // two blocks ahead) and the next fill of its stage
+    for (int i = 0; i < C::kStages && i < blocks; ++i) fetch(i, i);
+    float b0 = bias_at(0, lane), b1 = bias_at(0, lane + 32);
+    float c0 = bias_at(1, lane), c1 = bias_at(1, lane + 32);
+    int s = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < blocks; ++i) {
+      if (((i + 2) * n_box) >> 5 > grp0) {
+        ++grp0;
+        cur = nxt;
+        nxt = load_group(grp0 + 1);
+      }
+      const float d0 = bias_at(i + 2, lane), d1 = bias_at(i + 2, lane + 32);
+      s_bias[s][lane] = b0;
+      s_bias[s][lane + 32] = b1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[s]);
+      if (i + C::kStages < blocks) {
+        if (!mbar_wait_warp(&empty[s], ph, a.err)) break;
+        fetch(i + C::kStages, s);
+      }
+      b0 = c0;
+      b1 = c1;
+      c0 = d0;
+      c1 = d1;
+      if (++s == C::kStages) {
+        s = 0;
+        ph ^= 1u;
+      }
     }
   } else {
     // ------------------------------------------------------------ consumers
     uint32_t q[kDh / 16][4];
     float scale[2];
-    int64_t limit[2];
+    int limit[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const bool on = (lane >> 2) + 8 * i < n_rows;
-      const int h = g * group + static_cast<int>(row[i] % group);
+      const int h = g * group + row[i] % group;
       scale[i] = kLog2e / (sqrtf(static_cast<float>(kDh)) * (a.tau && on ? __ldg(a.tau + h) : 1.0f));
       gain2[i] = a.gain && a.kv.bias && on ? __ldg(a.gain + h) * kLog2e : 0.0f;
       limit[i] = on ? tile.past + row[i] / group + 1 : 0;
       const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                              (tile.tok0 + row[i] / group) * a.q_stride +
+                                                              static_cast<int64_t>(tile.tok0 + row[i] / group) * a.q_stride +
                                                               h * kDh) + (lane & 3);
 #pragma unroll
       for (int kk = 0; kk < kDh / 16; ++kk) {
@@ -237,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         mma16816(sc[1], q[kk], b[2], b[3]);
       }
       // logits in log2 units
-      const int64_t j0 = lo + static_cast<int64_t>(i) * kKeys + key0;
+      const int j0 = lo + i * kKeys + key0;
       uint32_t dead = 0, partial = 0;
       if (a.kv.bias != nullptr) {
         const float mine = s_bias[s][key0 + (lane & 15)];
@@ -258,14 +271,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       const bool edge = partial != 0 || j0 + 16 > min_limit;
       if (edge) {
-        const int64_t past_min = min_limit - j0, past_max = min(max_limit, hi) - j0;
+        const int past_min = min_limit - j0, past_max = min(max_limit, hi) - j0;
         if (past_min < 16) partial |= past_min <= 0 ? 0xFFFFu : (0xFFFFu << past_min) & 0xFFFFu;
         if (past_max < 16) dead = past_max <= 0 ? 0xFFFFu : (0xFFFFu << past_max) & 0xFFFFu;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int64_t j = j0 + t * 8 + (lane & 3) * 2 + (e & 1);
+            const int j = j0 + t * 8 + (lane & 3) * 2 + (e & 1);
             if (j >= limit[e >> 1] || j >= hi || sc[t][e] <= kMaskedLogit) sc[t][e] = -INFINITY;
           }
       }
@@ -343,18 +356,18 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (s_found) {
     // Infinite or NaN values of keys that only some rows see were left out:
     // each goes to the rows that see it.
-    for (int64_t j = lo; j < hi; ++j) {
+    for (int j = lo; j < hi; ++j) {
       const int64_t page = page_of(a, tile.req, j);
       if (page < 0) continue;
-      const float b = a.kv.bias ? key_bias(__ldg(a.kv.bias + page * a.kv.bias_page_stride + j % a.kv.page_size)) : 0.f;
+      const float b = a.kv.bias ? key_bias(__ldg(a.kv.bias + page * a.kv.bias_page_stride + row_in_page(a, j))) : 0.f;
       if (j < min_limit && !(b < kRemovableBias)) continue;
       const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.kv.v) + page * a.kv.v_page_stride +
-                               ((j % a.kv.page_size) * a.kv.hkv + g) * kDh;
+                               (static_cast<int64_t>(row_in_page(a, j)) * a.kv.hkv + g) * kDh;
       for (int d = threadIdx.x; d < kDh; d += kThreads) {
         const float f = __bfloat162float(v[d]);
         if (isfinite(f)) continue;
         for (int r = 0; r < n_rows; ++r) {
-          const int64_t rr = tile.row0 + r;
+          const int rr = tile.row0 + r;
           const float gn = a.gain ? __ldg(a.gain + g * group + rr % group) * kLog2e : 0.f;
           if (j < tile.past + rr / group + 1 && !(gn * b <= kMaskedLogit)) acc[r * kDh + d] += f;
         }
@@ -375,9 +388,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       const float4 f = *reinterpret_cast<const float4*>(acc + (w * kRows + r) * kDh + c);
       v = make_float4(v.x + f.x, v.y + f.y, v.z + f.z, v.w + f.w);
     }
-    const int64_t rr = tile.row0 + r;
+    const int rr = tile.row0 + r;
     const int64_t t = tile.tok0 + rr / group;
-    const int h = g * group + static_cast<int>(rr % group);
+    const int h = g * group + rr % group;
     if (a.splits > 1) {
       const int64_t at = (split * a.rows + t) * a.hq + h;
       if (c == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(top, sum);
@@ -394,29 +407,32 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // ---------------------------------------------------------------- merge
-// One warp per (row, head): the splits' unnormalised outputs with weights
-// 2^(m_s - max m), in split order. A split without keys for the row has sum 0
-// and its output is not read.
-template <int kDh>
+// kWarps warps per (row, head): the splits' unnormalised outputs with weights
+// 2^(m_s - max m); warp w adds up splits w, w + kWarps, ... in order, and the
+// warps' sums are added in order. A split without keys for the row has sum 0
+// and its output is not read. One warp a row where there are few splits; with
+// many of them (few rows then) eight, so that they arrive together.
+template <int kDh, int kWarps>
 __global__ void __launch_bounds__(256) paged_merge(const __grid_constant__ PagedAttnArgs a) {
+  __shared__ float s_acc[kWarps > 1 ? kWarps : 1][kDh];
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t idx = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int64_t t = idx / a.hq;
-  const int h = static_cast<int>(idx % a.hq);
+  const int lane = threadIdx.x & 31, warp = static_cast<int>(threadIdx.x >> 5);
+  const int sub = warp % kWarps;  // this warp's share of the splits
+  const int idx = static_cast<int>(blockIdx.x) * (8 / kWarps) + warp / kWarps;
+  const int t = idx / a.hq, h = idx % a.hq;
   // rows behind the last request are left alone
   if (t >= a.rows || t < __ldg(a.cu_q) || t >= __ldg(a.cu_q + a.batch)) return;
   constexpr int kN = kDh / 32;
   const int64_t step = a.rows * a.hq;
   float m0 = -INFINITY, l0 = 0.f, m1 = -INFINITY, l1 = 0.f;
   if (lane < a.splits) {
-    const float2 v = *reinterpret_cast<const float2*>(a.part_ml + (lane * step + idx) * 2);
+    const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (lane * step + idx) * 2));
     m0 = v.x;
     l0 = v.y;
   }
   if (lane + 32 < a.splits) {
-    const float2 v = *reinterpret_cast<const float2*>(a.part_ml + ((lane + 32) * step + idx) * 2);
+    const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_ml + ((lane + 32) * step + idx) * 2));
     m1 = v.x;
     l1 = v.y;
   }
@@ -428,34 +444,65 @@ __global__ void __launch_bounds__(256) paged_merge(const __grid_constant__ Paged
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   float acc[kN] = {};
-  const float* src = a.part_o + idx * kDh + lane * kN;
+  const float* src = a.part_o + static_cast<int64_t>(idx) * kDh + lane * kN;
   const unsigned live0 = __ballot_sync(0xFFFFFFFFu, l0 != 0.f);
   const unsigned live1 = __ballot_sync(0xFFFFFFFFu, l1 != 0.f);
-#pragma unroll 4
-  for (int s = 0; s < a.splits; ++s) {
-    const float w = __shfl_sync(0xFFFFFFFFu, s < 32 ? w0 : w1, s & 31);
-    if (((s < 32 ? live0 : live1) >> (s & 31)) & 1u) {
+  // eight rows in flight at a time
+  for (int s0 = sub; s0 < a.splits; s0 += 8 * kWarps) {
+    float v[8][kN];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int s = s0 + i * kWarps;
+      const bool live = s < a.splits && (((s < 32 ? live0 : live1) >> (s & 31)) & 1u);
       const float* p = src + static_cast<int64_t>(s) * step * kDh;
       if constexpr (kN == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        acc[0] = fmaf(v.x, w, acc[0]);
-        acc[1] = fmaf(v.y, w, acc[1]);
-        acc[2] = fmaf(v.z, w, acc[2]);
-        acc[3] = fmaf(v.w, w, acc[3]);
+        const float4 f = live ? __ldcg(reinterpret_cast<const float4*>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[i][0] = f.x;
+        v[i][1] = f.y;
+        v[i][2] = f.z;
+        v[i][3] = f.w;
       } else {
-        const float2 v = *reinterpret_cast<const float2*>(p);
-        acc[0] = fmaf(v.x, w, acc[0]);
-        acc[1] = fmaf(v.y, w, acc[1]);
+        const float2 f = live ? __ldcg(reinterpret_cast<const float2*>(p)) : make_float2(0.f, 0.f);
+        v[i][0] = f.x;
+        v[i][1] = f.y;
       }
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int s = s0 + i * kWarps;
+      const float w = __shfl_sync(0xFFFFFFFFu, s < 32 ? w0 : w1, s & 31);
+      if (s < a.splits) {
+#pragma unroll
+        for (int e = 0; e < kN; ++e) acc[e] = fmaf(v[i][e], w, acc[e]);
+      }
+    }
+  }
+  if constexpr (kWarps > 1) {  // (the whole block has one row: no warp left above)
+#pragma unroll
+    for (int e = 0; e < kN; ++e) s_acc[sub][lane * kN + e] = acc[e];
+    __syncthreads();
+    if (sub != 0) return;
+#pragma unroll
+    for (int e = 0; e < kN; ++e)
+      for (int w = 1; w < kWarps; ++w) acc[e] += s_acc[w][lane * kN + e];
   }
   const bool any = sum != 0.f;
   const float inv = any ? 1.0f / sum : 0.f;
   if (lane == 0 && a.lse != nullptr)
     a.lse[h * a.rows + t] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + idx * kDh + lane * kN);
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) +
+                                              static_cast<int64_t>(idx) * kDh + lane * kN);
 #pragma unroll
   for (int e = 0; e < kN / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+}
+
+template <int kDh>
+cudaError_t merge(const PagedAttnArgs& a, cudaStream_t st) {
+  const int64_t n = a.rows * a.hq;
+  // (4096 keys in 33 splits, 16 rows: 13.1 us with one warp, 4.7 with eight)
+  if (a.splits <= 2 || (a.splits <= 8 && n > 16 * num_sms()))
+    return launch_pdl(paged_merge<kDh, 1>, dim3(static_cast<unsigned>((n + 7) / 8)), dim3(256), 0, st, a);
+  return launch_pdl(paged_merge<kDh, 8>, dim3(static_cast<unsigned>(n)), dim3(256), 0, st, a);
 }
 
 template <int kDh>
@@ -478,9 +525,7 @@ cudaError_t run(const PagedAttnArgs& a, int64_t tiles, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_paged_merge(const PagedAttnArgs& a, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>((a.rows * a.hq + 7) / 8);
-  return a.kv.dh == 128 ? launch_pdl(paged_merge<128>, dim3(grid), dim3(256), 0, st, a)
-                        : launch_pdl(paged_merge<64>, dim3(grid), dim3(256), 0, st, a);
+  return a.kv.dh == 128 ? merge<128>(a, st) : merge<64>(a, st);
 }
 
 cudaError_t launch_paged_decode(PagedAttnArgs a, void* ws, cudaStream_t st) {
@@ -495,6 +540,7 @@ cudaError_t launch_paged_decode(PagedAttnArgs a, void* ws, cudaStream_t st) {
   if (chunk > 2048) chunk = 2048;
   chunk = std::max<int64_t>(chunk, (a.max_kv + most - 1) / most);
   a.chunk = (chunk + kKeys - 1) / kKeys * kKeys;
+  a.chunk0 = a.chunk;
   a.splits = static_cast<int>((a.max_kv + a.chunk - 1) / a.chunk);
   paged_partials(&a, ws);
   const cudaError_t e = a.kv.dh == 128 ? run<128>(a, tiles, st) : run<64>(a, tiles, st);

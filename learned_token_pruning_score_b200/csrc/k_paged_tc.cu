@@ -1,0 +1,767 @@
+// k_paged_tc.cu -- tg_paged_attn for chunks of new tokens, bf16, on the
+// 5th-generation tensor cores (tcgen05, sm_100a).
+//
+// A row is a (token, query head of the KV head's group) pair, token-major. One
+// CTA takes up to 256 rows of a request and KV head over one split of its keys,
+// in 128-key tiles that TMA gathers from the pages (a box per page piece and 64
+// columns, 128-byte swizzle). Two softmax warpgroups (A, B) take turns with the
+// tensor core, as in the contiguous kernel (k_attn_tc.cu):
+//   over 128 rows   A holds rows 0 .. 127, B rows 128 .. 255; both read every tile
+//   up to 128 rows  both hold the same rows; A takes the even tiles, B the odd
+//                   ones, and the two states merge at the end, so that short
+//                   chunks (drafted tokens) keep the tensor core and the loads as
+//                   busy
+// Warps: 0 fetches K and V (lanes walk the page table two tiles ahead), 1 issues
+// the MMAs, 2 allocates TMEM and prepares the keys' gate biases, 3 cleans value
+// rows that must not reach a row, 4-7 softmax A, 8-11 softmax B (one thread a
+// row).
+//
+// Per tile and warpgroup: S = Q K^T into 128 TMEM columns, P (bf16) written over
+// S, O += P V with P read from TMEM and V as it lies in the page (keys as K, dh
+// as the contiguous MN dimension): no transposed copy. The order PV(j), QK(j + 1)
+// per warpgroup means that S(j + 1) is seen only after PV(j) has finished, so O
+// may be rescaled and P overwritten without another wait.
+//
+// Gate bias: one more 16-wide K-step adds g b with g = gain sqrt(dh) tau, each
+// of g and b in three bf16 parts and the six products down to 2^-24 kept. Keys
+// whose bias is below -1e20 get b = 0 there and are decided one by one in fp32.
+//
+// Value rows: a weight of zero does not hide an infinity or a NaN from the
+// matrix product. Rows behind the request's end are cleared in shared memory
+// (they were never written); infinities and NaN of keys that only some rows see
+// (the chunk's own tokens, keys removed by their bias) are cleared, noted, and
+// added at the end to the rows that do see them.
+#include <algorithm>
+#include <atomic>
+
+#include "tg_device.cuh"
+#include "tg_internal.h"
+#include "tg_paged.cuh"
+
+namespace tg {
+namespace {
+
+constexpr int kBlk = 128;          // rows of a warpgroup = keys of a tile
+constexpr int kThreads = 384;
+constexpr int kSub = 128 * 128;    // [128 rows x 64 bf16], 128-byte swizzle
+constexpr int kAugTile = 128 * 32; // [128 rows x 16 bf16], 32-byte swizzle
+constexpr float kRescale = 8.0f;   // log2 units
+// Register split (setmaxnreg), as in k_attn_tc.cu: it must use exactly the
+// registers the CTA launched with; the launcher checks the compiled count.
+constexpr uint32_t kRegsLaunch = 168, kRegsLow = 72, kRegsHigh = 216;
+static_assert(kRegsLow * 128 + kRegsHigh * 256 == kRegsLaunch * kThreads, "register split");
+
+template <int kDh>
+struct Lay {
+  static constexpr int kSubs = kDh / 64;
+  static constexpr int kTile = kSubs * kSub;         // [128 x kDh] bf16
+  static constexpr int kOffQAug = 0;                 // A, B
+  static constexpr int kOffKAug = 2 * kAugTile;      // 4 stages
+  static constexpr int kOffQ = 6 * kAugTile;         // A, B
+  static constexpr int kOffK = kOffQ + 2 * kTile;    // 2 stages
+  static constexpr int kOffV = kOffK + 2 * kTile;    // 2 stages
+  static constexpr int kOffBias = kOffV + 2 * kTile; // 4 x 128 fp32
+  static constexpr int kOffMask = kOffBias + 4 * 512;
+  static constexpr int kOffBar = kOffMask + 64;
+  static constexpr size_t kSmem = 1024 + kOffBar + 256;
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+  // B's output rows wait for the merge in the (by then idle) K tiles
+  static_assert(128 * kDh * 4 == 2 * kTile, "merge buffer");
+};
+
+constexpr uint32_t idesc_bmn(int m, int n) { return idesc_bf16_f32(m, n) | (1u << 16); }
+
+// MN-major operand, 128-byte swizzle: 128-byte rows of 64 MN elements, one K
+// index each, 8-row groups 1024 bytes apart, 64-element MN blocks `lbo` apart.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t addr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// 2^x for a pair on the FMA pipe, x <= 8: x = j + f with j = round(x) (adding
+// 1.5 * 2^23 leaves it in the low mantissa bits), a degree-3 polynomial for
+// 2^f, |f| <= 1/2, fitted here with p(0) = 1 (largest relative error 1.02e-4),
+// and j added to the exponent field. Below -127 that gives exactly 0, so a
+// masked logit (-inf) has no weight; a NaN comes out as 3e38 (infinity in
+// bf16) and so still shows in the output.
+__device__ __forceinline__ float2 exp2_fma(float2 x) {
+  x.x = max_nan(x.x, -127.0f);
+  x.y = max_nan(x.y, -127.0f);
+  const float2 kShift = make_float2(12582912.0f, 12582912.0f);
+  const float2 t = fadd2(x, kShift);
+  const float2 f = fadd2(x, fadd2(make_float2(-t.x, -t.y), kShift));
+  float2 p = ffma2(f, make_float2(0.0550089329f, 0.0550089329f), make_float2(0.242210999f, 0.242210999f));
+  p = ffma2(p, f, make_float2(0.693282902f, 0.693282902f));
+  p = ffma2(p, f, make_float2(1.0f, 1.0f));
+  return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
+                     __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+}
+
+// x in three bf16 parts (each the rest of the one before)
+__device__ __forceinline__ void split3(float x, float& p0, float& p1, float& p2) {
+  p0 = __bfloat162float(__float2bfloat16_rn(x));
+  p1 = __bfloat162float(__float2bfloat16_rn(x - p0));
+  p2 = x - p0 - p1;
+}
+// Row r of a 32-byte-swizzled [128 x 16] tile: 16-byte unit c sits at c ^ (r >> 2 & 1).
+__device__ __forceinline__ void store_aug(uint8_t* tile, int r, uint32_t a, uint32_t b, uint32_t c) {
+  const int sw = (r >> 2) & 1;
+  *reinterpret_cast<uint4*>(tile + r * 32 + (sw << 4)) = make_uint4(a, b, c, 0u);
+  *reinterpret_cast<uint4*>(tile + r * 32 + ((1 ^ sw) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Clears the infinities and NaN among 8 bf16 values.
+__device__ __forceinline__ bool clear_nonfinite(uint4& u) {
+  bool any = false;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7F80u) == 0x7F80u) {
+      w[i] &= 0xFFFF0000u;
+      any = true;
+    }
+    if ((w[i] & 0x7F800000u) == 0x7F800000u) {
+      w[i] &= 0x0000FFFFu;
+      any = true;
+    }
+  }
+  return any;
+}
+
+template <int kDh, bool kBias>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const __grid_constant__ PagedAttnArgs a) {
+  using L = Lay<kDh>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  float* s_bias = reinterpret_cast<float*>(smem + L::kOffBias);        // [4][128]
+  uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + L::kOffMask);  // [4][4]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint64_t* q_full = bars + 0;
+  uint64_t* k_full = bars + 1;    // [2]
+  uint64_t* k_empty = bars + 3;   // [2]
+  uint64_t* v_full = bars + 5;    // [2] the bytes are there
+  uint64_t* v_ready = bars + 7;   // [2] and cleaned
+  uint64_t* v_empty = bars + 9;   // [2]
+  uint64_t* s_full = bars + 11;   // [A, B]
+  uint64_t* p_full = bars + 13;   // [A, B]
+  uint64_t* o_full = bars + 15;   // [A, B]
+  uint64_t* b_full = bars + 17;   // [4] biases and mask of a tile
+  uint64_t* b_empty = bars + 21;  // [4]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 25);
+  __shared__ PagedTile s_tile;
+  __shared__ int s_found;
+  __shared__ float2 s_ml[kBlk];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tile_idx = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.tiles));
+  const int rest = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.tiles));
+  const int g = rest % a.kv.hkv, split = rest / a.kv.hkv;
+  const int group = a.hq / a.kv.hkv;
+
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 256);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_ready[i], 1);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_full[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&b_full[i], 1);
+      mbar_init(&b_empty[i], 1);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    s_found = 0;
+  }
+  pdl_wait();
+  if (warp == 0) {
+    const PagedTile t = find_tile(a, 2 * kBlk, tile_idx);
+    if (lane == 0) s_tile = t;
+  }
+  __syncthreads();
+  const PagedTile tile = s_tile;
+  if (tile.req < 0) return;
+  const int n_rows = min(2 * kBlk, tile.n * group - tile.row0);
+  const bool dual = n_rows <= kBlk;
+  const int row0 = tile.row0, past = tile.past;
+  // keys that the first and the last row of the tile see, and this CTA's keys
+  const int min_limit = past + row0 / group + 1;
+  const int max_limit = past + (row0 + n_rows - 1) / group + 1;
+  const int64_t lo64 = split == 0 ? 0 : a.chunk0 + (split - 1) * a.chunk;
+  const int64_t hi64 = min(static_cast<int64_t>(max_limit), lo64 + (split == 0 ? a.chunk0 : a.chunk));
+  const int nt = hi64 > lo64 ? static_cast<int>((hi64 - lo64 + kBlk - 1) / kBlk) : 0;
+  const int lo = static_cast<int>(lo64), hi = static_cast<int>(hi64);
+  // output row of row r of the tile: (token, head)
+  auto out_row = [&](int r) -> int64_t {
+    const int rr = row0 + r;
+    return static_cast<int64_t>(tile.tok0 + rr / group) * a.hq + g * group + rr % group;
+  };
+  if (nt == 0) {  // nothing to see
+    for (int r = threadIdx.x; r < n_rows; r += kThreads) {
+      const int64_t at = out_row(r);
+      if (a.splits > 1) {
+        *reinterpret_cast<float2*>(a.part_ml + (split * a.rows * a.hq + at) * 2) =
+            make_float2(-INFINITY, 0.f);
+      } else {
+        uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * kDh);
+        for (int i = 0; i < kDh / 8; ++i) out[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.lse != nullptr) a.lse[(at % a.hq) * a.rows + at / a.hq] = -INFINITY;
+      }
+    }
+    return;
+  }
+  if (warp == 2) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // tiles of the two warpgroups
+  const int n_h[2] = {dual ? (nt + 1) / 2 : nt, dual ? nt / 2 : nt};
+
+  if (warp < 4) {
+    setmaxnreg_dec<kRegsLow>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ TMA
+      const int page = a.kv.page_size;
+      const int box = min(page, kBlk);       // rows of a box
+      const int n_box = kBlk / box;          // a power of two
+      const int my_box = lane & (n_box - 1), my_sub = lane / n_box;
+      const bool mine = my_sub < L::kSubs;
+      auto page_at = [&](int t) -> int {  // -1: behind the keys; n_pages: reads zeros
+        const int j = lo + t * kBlk + my_box * box;
+        if (t >= nt || j >= hi) return -1;
+        const int64_t p = page_of(a, tile.req, j);
+        return p < 0 ? static_cast<int>(a.kv.n_pages) : static_cast<int>(p);
+      };
+      int pg = page_at(0), pg1 = page_at(1);
+      for (int t = 0; t < nt; ++t) {
+        const int s = t & 1;
+        const uint32_t ph = ((t >> 1) & 1) ^ 1;
+        const int pg2 = page_at(t + 2);
+        const bool go = mine && pg >= 0;
+        const uint32_t bytes =
+            static_cast<uint32_t>(__popc(__ballot_sync(0xFFFFFFFFu, go)) * box * 128);
+        const int y = row_in_page(a, lo + t * kBlk + my_box * box);
+        const int off = my_sub * kSub + my_box * box * 128;
+        if (!mbar_wait_warp(&k_empty[s], ph, a.err)) break;
+        if (lane == 0) mbar_arrive_expect_tx(&k_full[s], bytes);
+        __syncwarp();
+        if (go) tma_load_4d(&tmK, &k_full[s], smem + L::kOffK + s * L::kTile + off, my_sub * 64, g, y, pg);
+        if (!mbar_wait_warp(&v_empty[s], ph, a.err)) break;
+        if (lane == 0) mbar_arrive_expect_tx(&v_full[s], bytes);
+        __syncwarp();
+        if (go) tma_load_4d(&tmV, &v_full[s], smem + L::kOffV + s * L::kTile + off, my_sub * 64, g, y, pg);
+        pg = pg1;
+        pg1 = pg2;
+      }
+    } else if (warp == 1 && lane == 0) {
+      // ------------------------------------------------------------ MMA
+      auto qk = [&](int h, int t) {
+        constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
+        const uint32_t q_addr = smem_addr(smem + L::kOffQ + (h && !dual ? L::kTile : 0));
+        const uint32_t k_addr = smem_addr(smem + L::kOffK + (t & 1) * L::kTile);
+        const uint32_t d = tmem + static_cast<uint32_t>(h * 128);
+#pragma unroll
+        for (int kk = 0; kk < kDh / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kSub + (kk & 3) * 32;
+          umma_f16_ss(d, sdesc_kmajor_sw128(q_addr + off), sdesc_kmajor_sw128(k_addr + off), idesc,
+                      kk > 0 ? 1u : 0u);
+        }
+        if (kBias)
+          umma_f16_ss(d, sdesc_kmajor_sw32(smem_addr(smem + L::kOffQAug + (h && !dual ? kAugTile : 0))),
+                      sdesc_kmajor_sw32(smem_addr(smem + L::kOffKAug + (t & 3) * kAugTile)), idesc, 1u);
+        umma_commit(&s_full[h]);
+        if (h == 1 || dual) umma_commit(&k_empty[t & 1]);
+      };
+      auto pv = [&](int h, int t, bool first) {
+        constexpr uint32_t idesc = idesc_bmn(128, kDh);
+        const uint32_t v_addr = smem_addr(smem + L::kOffV + (t & 1) * L::kTile);
+        const uint32_t p_tm = tmem + static_cast<uint32_t>(h * 128);
+        const uint32_t d = tmem + 256u + static_cast<uint32_t>(h * 128);
+#pragma unroll
+        for (int kk = 0; kk < kBlk / 16; ++kk)
+          umma_f16_ts(d, p_tm + static_cast<uint32_t>(kk * 8), sdesc_mn(v_addr + kk * 2048, kSub), idesc,
+                      (!first || kk > 0) ? 1u : 0u);
+      };
+      auto k_there = [&](int t) -> bool {
+        return mbar_wait(&k_full[t & 1], (t >> 1) & 1, a.err) &&
+               (!kBias || mbar_wait(&b_full[t & 3], (t >> 2) & 1, a.err));
+      };
+      bool ok = mbar_wait(q_full, 0, a.err) && k_there(0);
+      if (ok) {
+        tc_fence_after();
+        qk(0, 0);
+        if (n_h[1] > 0) {
+          if (dual) ok = k_there(1);
+          tc_fence_after();
+          if (ok) qk(1, dual ? 1 : 0);
+        }
+      }
+      for (int j = 0; j < n_h[0] && ok; ++j) {
+#pragma unroll 1
+        for (int h = 0; h < 2 && ok; ++h) {
+          if (j >= n_h[h]) break;
+          const int t = dual ? 2 * j + h : j;
+          if (h == 0 || dual) ok = mbar_wait(&v_ready[t & 1], (t >> 1) & 1, a.err);
+          ok = ok && mbar_wait(&p_full[h], j & 1, a.err);
+          if (!ok) break;
+          tc_fence_after();
+          pv(h, t, j == 0);
+          if (j + 1 == n_h[h]) umma_commit(&o_full[h]);
+          if (h == 1 || dual) {
+            umma_commit(&v_empty[t & 1]);
+            if (kBias) umma_commit(&b_empty[t & 3]);  // both softmaxes have read the mask
+          }
+          if (j + 1 < n_h[h]) {
+            const int tk = dual ? t + 2 : j + 1;
+            if (h == 0 || dual) ok = k_there(tk);
+            if (!ok) break;
+            tc_fence_after();
+            qk(h, tk);
+          }
+        }
+      }
+    } else if (warp == 2 && kBias) {
+      // ------------------------------------------------------------ gate biases
+      // four keys a lane: lane, lane + 32, ...; pages two tiles ahead, biases one
+      auto page_at = [&](int t, int i) -> int64_t {
+        const int j = lo + t * kBlk + lane + 32 * i;
+        return t < nt && j < hi ? page_of(a, tile.req, j) : -1;
+      };
+      auto bias_at = [&](int t, int i, int64_t p) -> float {
+        if (p < 0) return 0.f;
+        return __ldg(a.kv.bias + p * a.kv.bias_page_stride + row_in_page(a, lo + t * kBlk + lane + 32 * i));
+      };
+      float b[4];
+      int64_t pg[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        b[i] = bias_at(0, i, page_at(0, i));
+        pg[i] = page_at(1, i);
+      }
+      for (int t = 0; t < nt; ++t) {
+        float nb[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          nb[i] = bias_at(t + 1, i, pg[i]);
+          pg[i] = page_at(t + 2, i);
+        }
+        if (!mbar_wait_warp(&b_empty[t & 3], ((t >> 2) & 1) ^ 1, a.err)) break;
+        uint8_t* tile_aug = smem + L::kOffKAug + (t & 3) * kAugTile;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = lane + 32 * i;
+          const bool rem = b[i] < kRemovableBias;
+          const unsigned bits = __ballot_sync(0xFFFFFFFFu, rem);
+          if (lane == 0) s_mask[(t & 3) * 4 + i] = bits;
+          s_bias[(t & 3) * 128 + r] = key_bias(b[i]);
+          float b0, b1, b2;
+          split3(rem ? 0.f : b[i], b0, b1, b2);
+          // against (g0, g0, g1, g0, g2, g1)
+          store_aug(tile_aug, r, pack_bf16x2(b0, b1), pack_bf16x2(b0, b2), pack_bf16x2(b0, b1));
+          b[i] = nb[i];
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_full[t & 3]);
+      }
+    } else if (warp == 3) {
+      // ------------------------------------------------------------ values
+      for (int t = 0; t < nt; ++t) {
+        const int key0 = lo + t * kBlk;
+        uint4 part = make_uint4(0u, 0u, 0u, 0u);  // keys that their bias may remove
+        if (kBias) {
+          if (!mbar_wait_warp(&b_full[t & 3], (t >> 2) & 1, a.err)) break;
+          part = *reinterpret_cast<const uint4*>(s_mask + (t & 3) * 4);
+        }
+        const int s = t & 1;
+        if (!mbar_wait_warp(&v_full[s], (t >> 1) & 1, a.err)) break;
+        if ((part.x | part.y | part.z | part.w) != 0u || key0 + kBlk > min_limit) {
+          uint8_t* v = smem + L::kOffV + s * L::kTile;
+          constexpr int kUnits = kDh / 8;  // 16-byte units of a row
+          bool found = false;
+          for (int e = lane; e < kBlk * kUnits; e += 32) {
+            const int r = e / kUnits, u = e % kUnits;
+            const bool dead = key0 + r >= hi;
+            const unsigned word = r < 32 ? part.x : r < 64 ? part.y : r < 96 ? part.z : part.w;
+            if (!dead && key0 + r < min_limit && !((word >> (r & 31)) & 1u)) continue;
+            uint4* at = reinterpret_cast<uint4*>(v + (u >> 3) * kSub + r * 128 + (((u & 7) ^ (r & 7)) << 4));
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (!dead) {
+              x = *at;
+              if (!clear_nonfinite(x)) continue;
+              found = true;
+            }
+            *at = x;
+          }
+          if (found) s_found = 1;
+          fence_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_ready[s]);
+      }
+    }
+  } else {
+    setmaxnreg_inc<kRegsHigh>();
+    // -------------------------------------------------------------- softmax
+    const int h = (warp - 4) >> 2;            // warpgroup A or B
+    const int r = (threadIdx.x - 128) & 127;  // row of the warpgroup = TMEM lane
+    const int rt = (dual ? 0 : h * kBlk) + r; // row of the tile
+    const bool row_ok = rt < n_rows;
+    const int head = g * group + (row0 + rt) % group;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_tm = tmem + lane_off + static_cast<uint32_t>(h * 128);
+    const uint32_t o_tm = tmem + lane_off + 256u + static_cast<uint32_t>(h * 128);
+    const float tau = a.tau && row_ok ? __ldg(a.tau + head) : 1.0f;
+    const float gain = kBias && row_ok ? __ldg(a.gain + head) : 0.0f;
+    const float scale2 = kLog2e / (sqrtf(static_cast<float>(kDh)) * tau);
+    // rows without a query see everything (their output goes nowhere)
+    const int limit = row_ok ? past + (row0 + rt) / group + 1 : 0x7FFFFFFF;
+    if (!dual || h == 0) {  // this warpgroup's rows of Q, 16 bytes a thread and step
+      uint8_t* qd = smem + L::kOffQ + (dual ? 0 : h * L::kTile);
+      constexpr int kUnits = kDh / 8;
+#pragma unroll 4
+      for (int e = r; e < kBlk * kUnits; e += kBlk) {
+        const int qr = e / kUnits, u = e % kUnits;
+        const int rr = (dual ? 0 : h * kBlk) + qr;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (rr < n_rows)
+          x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                              static_cast<int64_t>(tile.tok0 + (row0 + rr) / group) * a.q_stride +
+                                              (g * group + (row0 + rr) % group) * kDh + u * 8);
+        *reinterpret_cast<uint4*>(qd + (u >> 3) * kSub + qr * 128 + (((u & 7) ^ (qr & 7)) << 4)) = x;
+      }
+      if (kBias) {
+        float g0, g1, g2;
+        split3(gain * sqrtf(static_cast<float>(kDh)) * tau, g0, g1, g2);
+        store_aug(smem + L::kOffQAug + (dual ? 0 : h * kAugTile), r, pack_bf16x2(g0, g0),
+                  pack_bf16x2(g1, g0), pack_bf16x2(g2, g1));
+      }
+      fence_async_smem();
+    }
+    mbar_arrive(q_full);
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n_h[h] && ok; ++j) {
+      const int t = dual ? 2 * j + h : j;
+      const int key0 = lo + t * kBlk;
+      if (!mbar_wait_warp(&s_full[h], j & 1, a.err)) { ok = false; break; }
+      tc_fence_after();
+      // Tiles that hold keys some row of the warp must not see, or keys that
+      // their bias may remove (then decided in fp32): their logits are put
+      // right in TMEM first, 32 at a time, so that the loop's own code, which
+      // is all that most tiles run, stays small enough for the instruction
+      // cache (with the masks inlined in it: 740 us, so 625, for 2048 tokens
+      // after 30720).
+      uint4 rem = make_uint4(0u, 0u, 0u, 0u);
+      if (kBias) {
+        if (!mbar_wait_warp(&b_full[t & 3], (t >> 2) & 1, a.err)) { ok = false; break; }
+        rem = *reinterpret_cast<const uint4*>(s_mask + (t & 3) * 4);
+      }
+      if (__any_sync(0xFFFFFFFFu, key0 + kBlk > limit) || (rem.x | rem.y | rem.z | rem.w) != 0u) {
+        const float* bs = s_bias + (t & 3) * 128;
+        const float gs = gain * sqrtf(static_cast<float>(kDh)) * tau;
+        const float floor_x = kMaskedLogit / scale2;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float z[32];
+          tmem_ld32_wait(s_tm + static_cast<uint32_t>(c * 32), z);
+          const uint32_t word = c == 0 ? rem.x : c == 1 ? rem.y : c == 2 ? rem.z : rem.w;
+          const int seen = limit - key0 - c * 32;  // of these 32 keys
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (kBias && ((word >> i) & 1u)) {
+              z[i] = fmaf(gs, bs[c * 32 + i], z[i]);
+              if (z[i] <= floor_x) z[i] = -INFINITY;
+            }
+            if (i >= seen) z[i] = -INFINITY;
+          }
+          tmem_st32_wait(s_tm + static_cast<uint32_t>(c * 32), z);
+        }
+      }
+      float x[128];
+      {
+        uint32_t r0[32], r1[32], r2[32], r3[32];
+        tmem_ld32(s_tm, r0);
+        tmem_ld32(s_tm + 32, r1);
+        tmem_ld32(s_tm + 64, r2);
+        tmem_ld32(s_tm + 96, r3);
+        tmem_wait_ld_dep(r3);
+        tmem_ld_fence(r0);
+        tmem_ld_fence(r1);
+        tmem_ld_fence(r2);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          x[i] = __uint_as_float(r0[i]);
+          x[32 + i] = __uint_as_float(r1[i]);
+          x[64 + i] = __uint_as_float(r2[i]);
+          x[96 + i] = __uint_as_float(r3[i]);
+        }
+      }
+      // eight chains of 3-input maxima
+      float mx8[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mx8[k] = fmax3f(x[k], x[8 + k], x[16 + k]);
+#pragma unroll
+      for (int i = 24; i < 120; i += 16)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx8[k] = fmax3f(mx8[k], x[i + k], x[i + 8 + k]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(mx8[k], x[120 + k]);
+      const float mx = fmax3f(fmax3f(mx8[0], mx8[1], mx8[2]), fmax3f(mx8[3], mx8[4], mx8[5]),
+                              fmaxf(mx8[6], mx8[7])) *
+                       scale2;
+      float alpha = 1.0f;
+      if (mx > m + kRescale || (m == -INFINITY && mx != -INFINITY)) {
+        alpha = ex2_approx(m - mx);  // 0 on the first keys
+        l *= alpha;
+        m = mx;
+      }
+      const bool rescale_o = j > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.0f);
+      // P = 2^(S scale2 - m) in packed pairs, one pair in four on the FMA pipe
+      // (the MUFU unit is this loop's bottleneck)
+      const float base = m == -INFINITY ? 0.f : m;
+      float2 sp[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                      make_float2(0.f, 0.f)};
+      const float2 sc2 = make_float2(scale2, scale2), nm2 = make_float2(-base, -base);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float2 y = ffma2(make_float2(x[64 * half + 2 * i], x[64 * half + 2 * i + 1]), sc2, nm2);
+          float2 e;
+          if ((i & 3) == 3) {
+            e = exp2_fma(y);
+          } else {
+            e.x = ex2_approx(y.x);
+            e.y = ex2_approx(y.y);
+          }
+          sp[i & 3] = fadd2(sp[i & 3], e);
+          pk[i] = pack_bf16x2(e.x, e.y);
+        }
+        tmem_st32(s_tm + static_cast<uint32_t>(32 * half), pk);
+        tmem_wait_st();
+      }
+      const float2 s2 = fadd2(fadd2(sp[0], sp[1]), fadd2(sp[2], sp[3]));
+      l += s2.x + s2.y;
+      if (rescale_o) {
+#pragma unroll 1
+        for (int c = 0; c < kDh / 32; ++c) {
+          float o[32];
+          const uint32_t ta = o_tm + static_cast<uint32_t>(c * 32);
+          tmem_ld32_wait(ta, o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= alpha;
+          tmem_st32_wait(ta, o);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&p_full[h]);
+    }
+    // -------------------------------------------------------------- output
+    // With `dual`, B's rows wait in the idle K tiles for A's threads.
+    const bool active = !dual || h == 0;
+    ok = ok && (n_h[h] == 0 || mbar_wait_warp(&o_full[h], 0, a.err));
+    if (dual && h == 1) ok = ok && mbar_wait_warp(&o_full[0], 0, a.err);  // all MMAs have read K
+    // the last tile's values are cleaned: s_found is final
+    ok = ok && mbar_wait_warp(&v_ready[(nt - 1) & 1], ((nt - 1) >> 1) & 1, a.err);
+    tc_fence_after();
+    float4* xo = reinterpret_cast<float4*>(smem + L::kOffK) + r;  // [kDh / 4][128 rows]
+    float wa = 1.0f, wb = 0.f;
+    if (dual) {
+      if (h == 1) {
+        s_ml[r] = make_float2(m, ok ? l : 0.f);
+        if (ok && n_h[1] > 0) {
+#pragma unroll 1
+          for (int c = 0; c < kDh / 32; ++c) {
+            float o[32];
+            tmem_ld32_wait(o_tm + static_cast<uint32_t>(c * 32), o);
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              xo[(c * 8 + v) * 128] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+          }
+        }
+      }
+      named_bar_sync(1, 256);
+      if (h == 0) {
+        const float2 b = s_ml[r];
+        const float top = fmaxf(m, b.x);
+        wa = state_weight(m, l, top);
+        wb = state_weight(b.x, b.y, top);
+        m = top;
+        l = l * wa + b.y * wb;
+      }
+    }
+    if (active && ok) {
+      const bool part = a.splits > 1;
+      const bool any = l != 0.f;  // a row that sees nothing is zero
+      const float inv = part ? 1.0f : any ? 1.0f / l : 0.f;
+      if (row_ok) {
+        const int64_t at = out_row(rt);
+        if (part)
+          *reinterpret_cast<float2*>(a.part_ml + (split * a.rows * a.hq + at) * 2) = make_float2(m, l);
+        else if (a.lse != nullptr)
+          a.lse[head * a.rows + tile.tok0 + (row0 + rt) / group] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+      }
+      // each warp's 32 rows x 32 columns through its part of the idle Q tile
+      uint8_t* stage = smem + L::kOffQ + h * L::kTile + (warp & 3) * 4096;
+      const int found = *const_cast<volatile int*>(&s_found);
+#pragma unroll 1
+      for (int c = 0; c < kDh / 32; ++c) {
+        float o[32];
+        tmem_ld32_wait(o_tm + static_cast<uint32_t>(c * 32), o);
+        if (dual) {
+#pragma unroll
+          for (int v = 0; v < 8; ++v) {
+            const float4 b = wb != 0.f ? xo[(c * 8 + v) * 128] : make_float4(0.f, 0.f, 0.f, 0.f);
+            o[4 * v] = o[4 * v] * wa + b.x * wb;
+            o[4 * v + 1] = o[4 * v + 1] * wa + b.y * wb;
+            o[4 * v + 2] = o[4 * v + 2] * wa + b.z * wb;
+            o[4 * v + 3] = o[4 * v + 3] * wa + b.w * wb;
+          }
+        }
+        if (found && row_ok) {
+          for (int jj = lo; jj < min(hi, limit); ++jj) {
+            const int64_t p = page_of(a, tile.req, jj);
+            if (p < 0) continue;
+            const int in = row_in_page(a, jj);
+            const float b = kBias ? key_bias(__ldg(a.kv.bias + p * a.kv.bias_page_stride + in)) : 0.f;
+            const bool rem = b < kRemovableBias;
+            if ((jj < min_limit && !rem) || (rem && gain * kLog2e * b <= kMaskedLogit)) continue;
+            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.kv.v) + p * a.kv.v_page_stride +
+                                     (static_cast<int64_t>(in) * a.kv.hkv + g) * kDh + c * 32;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float f = __bfloat162float(v[i]);
+              if (!isfinite(f)) o[i] += f;
+            }
+          }
+        }
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+          *reinterpret_cast<float4*>(stage + lane * 128 + ((v ^ (lane & 7)) << 4)) =
+              make_float4(o[4 * v] * inv, o[4 * v + 1] * inv, o[4 * v + 2] * inv, o[4 * v + 3] * inv);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = i * 4 + (lane >> 3), u = lane & 7;
+          const float4 f = *reinterpret_cast<const float4*>(stage + rr * 128 + ((u ^ (rr & 7)) << 4));
+          const int ro = (dual ? 0 : h * kBlk) + (warp & 3) * 32 + rr;
+          if (ro < n_rows) {
+            const int64_t at = out_row(ro);
+            if (part)
+              *reinterpret_cast<float4*>(a.part_o + (split * a.rows * a.hq + at) * kDh + c * 32 + u * 4) = f;
+            else
+              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at * kDh + c * 32 + u * 4) =
+                  make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+// Splits of the keys, from the sizes that the host knows (requests may be
+// shorter). Times in microseconds, as measured per CTA: a 128-key tile of two
+// warpgroups, the fixed cost of a CTA, the merge with its partial rows.
+void plan(PagedAttnArgs* a) {
+  const int64_t sms = num_sms();
+  const int group = a->hq / a->kv.hkv;
+  const int64_t jobs = a->tiles * a->kv.hkv;
+  const int64_t nt = (a->max_kv + kBlk - 1) / kBlk;
+  const int64_t mean_rows = a->rows * group / (a->tiles > 0 ? a->tiles : 1);
+  const double tile_us = (mean_rows <= kBlk ? 1.1 : 2.2) * (a->kv.dh == 128 ? 1.0 : 0.8), cta_us = 7.0;
+  const double part_us = double(a->rows) * a->hq * a->kv.dh * 8.0 / 5.0e6;  // one split's, out and in
+  const int most = paged_max_splits(a->rows, a->batch, a->hq, a->kv.hkv, 2 * kBlk);
+  double best = 1e300;
+  for (int s = 1; s <= most && s <= nt; ++s) {
+    const int64_t c = (nt + s - 1) / s;
+    const double us = double((jobs * s + sms - 1) / sms) * (c * tile_us + cta_us) +
+                      (s > 1 ? 4.0 + s * part_us : 0.0);
+    if (us < best - 1e-9) {
+      best = us;
+      a->splits = static_cast<int>((nt + c - 1) / c);
+      a->chunk0 = a->chunk = c * kBlk;
+    }
+  }
+  // Jobs that leave SMs idle: those take the last tiles of all of them, k each.
+  if (jobs < sms && most >= 2) {
+    const int64_t k = (jobs + sms - jobs - 1) / (sms - jobs);
+    const double y = (nt * tile_us + cta_us * (1 - k)) / ((k + 1) * tile_us);
+    const int64_t tail = static_cast<int64_t>(y);
+    if (tail >= 1 && tail < nt) {
+      const double us = std::max((nt - tail) * tile_us + cta_us, k * (tail * tile_us + cta_us)) + 4.0 +
+                        2 * part_us;
+      if (us < best) {
+        a->splits = 2;
+        a->chunk0 = (nt - tail) * kBlk;
+        a->chunk = tail * kBlk;
+      }
+    }
+  }
+}
+
+template <int kDh, bool kBias>
+cudaError_t run(const PagedAttnArgs& a, cudaStream_t st) {
+  using L = Lay<kDh>;
+  CUtensorMap tk, tv;
+  const int box = a.kv.page_size < kBlk ? a.kv.page_size : kBlk;
+  if (!make_tmap_pages_bf16(&tk, a.kv.k, kDh, a.kv.hkv, a.kv.page_size, a.kv.n_pages,
+                            a.kv.k_page_stride, box) ||
+      !make_tmap_pages_bf16(&tv, a.kv.v, kDh, a.kv.hkv, a.kv.page_size, a.kv.n_pages,
+                            a.kv.v_page_stride, box))
+    return cudaErrorInvalidValue;
+  auto kern = paged_attn_tc<kDh, kBias>;
+  TG_CUDA_TRY(set_smem_attr_once(reinterpret_cast<const void*>(kern), static_cast<int>(L::kSmem)));
+  // With any other register count setmaxnreg.inc could block: refuse.
+  static std::atomic<int> regs_ok{0};
+  if (regs_ok.load() == 0) {
+    cudaFuncAttributes fa;
+    TG_CUDA_TRY(cudaFuncGetAttributes(&fa, reinterpret_cast<const void*>(kern)));
+    regs_ok.store(fa.numRegs == int(kRegsLaunch) ? 1 : -1);
+  }
+  if (regs_ok.load() < 0) return cudaErrorInvalidConfiguration;
+  const int64_t grid = a.tiles * a.splits * a.kv.hkv;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), L::kSmem, st, tk, tv, a);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tc(PagedAttnArgs a, void* ws, cudaStream_t st) {
+  a.tiles = paged_row_tiles(a.rows, a.batch, a.hq, a.kv.hkv, 2 * kBlk);
+  plan(&a);
+  paged_partials(&a, ws);
+  const bool bias = a.gain != nullptr && a.kv.bias != nullptr;
+  cudaError_t e;
+  if (a.kv.dh == 128) e = bias ? run<128, true>(a, st) : run<128, false>(a, st);
+  else e = bias ? run<64, true>(a, st) : run<64, false>(a, st);
+  if (e != cudaSuccess || a.splits == 1) return e;
+  return launch_paged_merge(a, st);
+}
+
+}  // namespace tg

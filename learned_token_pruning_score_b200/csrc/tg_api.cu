@@ -1948,7 +1948,8 @@ tg_status paged_view(const tg_paged_kv* c, const int32_t* cu_q, const int32_t* k
            TG_ERR_INVALID_ARG);
   TG_CHECK(c->bias == nullptr || c->bias_page_stride >= ps, TG_ERR_INVALID_ARG);
   *v = PagedKv{c->k, c->v, c->bias, c->table, c->n_pages, c->k_page_stride, c->v_page_stride,
-               c->bias_page_stride, c->table_stride, ps, c->n_heads_kv, c->head_dim};
+               c->bias_page_stride, c->table_stride, ps, c->n_heads_kv, c->head_dim,
+               ps == 16 ? 4 : ps == 32 ? 5 : ps == 64 ? 6 : ps == 128 ? 7 : 8};
   return TG_OK;
 }
 }  // namespace
@@ -1956,7 +1957,7 @@ tg_status paged_view(const tg_paged_kv* c, const int32_t* cu_q, const int32_t* k
 namespace tg {
 size_t paged_attn_ws_bytes(int64_t rows, int64_t batch, int hq, int hkv, int dh) {
   // one split writes the output itself
-  const size_t s = paged_max_splits(rows, batch, hq, hkv, 16);
+  const size_t s = paged_max_splits(rows, batch, hq, hkv, paged_tile_rows(rows, batch, hq, hkv));
   return s > 1 ? align_up(s * size_t(rows) * size_t(hq) * size_t(dh + 2) * 4, 256) : 256;
 }
 }  // namespace tg
@@ -2034,6 +2035,7 @@ tg_status tg_paged_attn(const tg_paged_kv* cache, const void* q, int64_t q_strid
            TG_ERR_INVALID_ARG);
   TG_CHECK(max_kv >= 1 && max_kv <= int64_t(cache->table_stride) * cache->page_size,
            TG_ERR_INVALID_ARG);
+  TG_CHECK(rows * hq < (int64_t(1) << 31) && max_kv <= (int64_t(1) << 30), TG_ERR_UNSUPPORTED);
   if (none) return TG_OK;
   a.q = q;
   a.q_stride = q_stride;
@@ -2056,7 +2058,9 @@ tg_status tg_paged_attn(const tg_paged_kv* cache, const void* q, int64_t q_strid
   const double bytes = 2.0 * rows * hq * dh * double(elem_size(dt));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return cuda_status(traced(TG_K_PAGED_ATTN, rows, 0.0, bytes, st, [&] {
-    return dt == TG_BF16 ? launch_paged_decode(a, ws, st) : launch_paged_attn_simt(a, st);
+    if (dt == TG_F32) return launch_paged_attn_simt(a, st);
+    return paged_tile_rows(rows, batch, hq, hkv) == 16 ? launch_paged_decode(a, ws, st)
+                                                       : launch_paged_tc(a, ws, st);
   }));
 }
 

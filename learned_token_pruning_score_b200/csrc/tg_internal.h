@@ -353,6 +353,7 @@ struct PagedKv {
   int64_t n_pages;
   int64_t k_page_stride, v_page_stride, bias_page_stride;  // elements between pages
   int table_stride, page_size, hkv, dh;
+  int page_shift;                   // page_size = 1 << page_shift
 };
 struct PagedAppendArgs {
   PagedKv kv;
@@ -384,23 +385,31 @@ struct PagedAttnArgs {
   void* out;                        // [rows, hq, dh]
   float* lse;                       // [hq, rows] or null
   unsigned int* err;
-  // split keys (bf16): split s covers keys [s chunk, (s + 1) chunk)
+  // bf16: the keys are split, [0, chunk0), then pieces of `chunk`
   int splits;
-  int64_t chunk;
+  int64_t chunk0, chunk;
+  int64_t tiles;                    // row tiles of the launch (upper bound)
   float* part_o;                    // [splits][rows][hq][dh], unnormalised
   float* part_ml;                   // [splits][rows][hq][2]: maximum (log2 units) and sum
 };
 // Upper bound of the row tiles of a call: rows are (token, head of the group)
 // pairs and each request's last tile may be short.
 inline int64_t paged_row_tiles(int64_t rows, int64_t batch, int hq, int hkv, int tile) {
-  return rows * (hq / hkv) / tile + (batch < rows ? batch : rows);
+  const int64_t requests = batch < rows ? batch : rows;
+  return (rows * (hq / hkv) - requests) / tile + requests;
+}
+// bf16: rows of a tile. Up to 16 rows of a request and KV head on average the
+// keys are what the call is made of (16, k_paged_decode.cu); above, the tensor
+// cores' tiles (256, k_paged_tc.cu).
+inline int paged_tile_rows(int64_t rows, int64_t batch, int hq, int hkv) {
+  return rows * (hq / hkv) <= 16 * batch ? 16 : 256;
 }
 // Most splits of a call: up to 64, while the (row tile, KV head, split) jobs
-// stay within 64 for each of 148 SMs, which also bounds the partial results
-// (of at most `tile` rows a job) whatever the batch.
+// stay within 64 (16 rows) or 4 (256 rows) for each of 148 SMs, which also
+// bounds the partial results whatever the batch.
 inline int paged_max_splits(int64_t rows, int64_t batch, int hq, int hkv, int tile) {
   const int64_t jobs = paged_row_tiles(rows, batch, hq, hkv, tile) * hkv;
-  const int64_t s = 64 * 148 / (jobs > 0 ? jobs : 1);
+  const int64_t s = (tile == 16 ? 64 : 4) * 148 / (jobs > 0 ? jobs : 1);
   return static_cast<int>(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 size_t paged_attn_ws_bytes(int64_t rows, int64_t batch, int hq, int hkv, int dh);
@@ -414,6 +423,8 @@ inline void paged_partials(PagedAttnArgs* a, void* ws) {
 cudaError_t launch_paged_attn_simt(const PagedAttnArgs& a, cudaStream_t st);
 // bf16: few rows a request (k_paged_decode.cu)
 cudaError_t launch_paged_decode(PagedAttnArgs a, void* ws, cudaStream_t st);
+// bf16: chunks (k_paged_tc.cu)
+cudaError_t launch_paged_tc(PagedAttnArgs a, void* ws, cudaStream_t st);
 cudaError_t launch_paged_merge(const PagedAttnArgs& a, cudaStream_t st);
 
 // ---- 8-bit integers (k_quant.cu)

@@ -21,51 +21,61 @@ constexpr float kRemovableBias = -1e20f;
 
 __device__ __forceinline__ float key_bias(float b) { return b < kLowestBias ? kLowestBias : b; }
 
+// Weight of a partial state (maximum m, sum l) under the maximum `top` of all.
+// A state without keys (l = 0) has none; one whose logits are all NaN has m =
+// -inf and l = NaN, and passes that on.
+__device__ __forceinline__ float state_weight(float m, float l, float top) {
+  return l == 0.f ? 0.f : ex2_approx(m - (top == -INFINITY ? 0.f : top));
+}
+
 // One tile of query rows of a request. A row is a (token, query head of the
-// KV head's group) pair: row r is token r / group, head r % group.
+// KV head's group) pair: row r is token r / group, head r % group. Rows and
+// keys are 32-bit (the call has fewer than 2^31 rows x heads).
 struct PagedTile {
-  int req;       // request, or -1: no such tile
-  int64_t tok0;  // first token of the request in q
-  int64_t n;     // its new tokens
-  int64_t past;  // cached rows before them (below 0 when kv_len < n)
-  int64_t row0;  // first row of the tile
+  int req;    // request, or -1: no such tile
+  int tok0;   // first token of the request in q
+  int n;      // its new tokens
+  int past;   // cached rows before them (below 0 when kv_len < n)
+  int row0;   // first row of the tile
 };
 
 // New tokens of request b, their first row in q, and the cached rows before
 // them; offsets or lengths that run out of range are cut (and reported).
-__device__ __forceinline__ void request_span(const PagedAttnArgs& a, int b, int64_t& lo, int64_t& n,
-                                             int64_t& past) {
+__device__ __forceinline__ void request_span(const PagedAttnArgs& a, int b, int& lo, int& n, int& past) {
   lo = __ldg(a.cu_q + b);
-  int64_t hi = __ldg(a.cu_q + b + 1);
-  int64_t len = __ldg(a.kv_len + b);
-  if (lo < 0 || hi < lo || hi > a.rows || len > a.max_kv) {
+  int hi = __ldg(a.cu_q + b + 1);
+  int len = __ldg(a.kv_len + b);
+  const int rows = static_cast<int>(a.rows);
+  const int max_kv = static_cast<int>(a.max_kv < 0x7FFFFFFF ? a.max_kv : 0x7FFFFFFF);
+  if (lo < 0 || hi < lo || hi > rows || len > max_kv) {
     report_error(a.err, kErrIndexRange);
     lo = lo < 0 ? 0 : lo;
-    hi = hi > a.rows ? a.rows : hi;
+    hi = hi > rows ? rows : hi;
     hi = hi < lo ? lo : hi;
-    len = len > a.max_kv ? a.max_kv : len;
+    len = len > max_kv ? max_kv : len;
   }
+  len = len < 0 ? 0 : len;  // no keys at all: as many rows as there are see nothing
   n = hi - lo;
   past = len - n;
 }
 
 // The idx-th tile of `rows_per_tile` rows, counted through the requests in
 // order. One full warp; every lane returns the same tile.
-__device__ __forceinline__ PagedTile find_tile(const PagedAttnArgs& a, int rows_per_tile, int64_t idx) {
+__device__ __forceinline__ PagedTile find_tile(const PagedAttnArgs& a, int rows_per_tile, int idx) {
   const int lane = static_cast<int>(threadIdx.x & 31);
   const int group = a.hq / a.kv.hkv;
-  int64_t before = 0;
+  int before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    int64_t lo = 0, n = 0, past = 0;
+    int lo = 0, n = 0, past = 0;
     if (b0 + lane < a.batch) request_span(a, b0 + lane, lo, n, past);
-    const int64_t cnt = (n * group + rows_per_tile - 1) / rows_per_tile;
-    int64_t sum = cnt;
+    const int cnt = (n * group + rows_per_tile - 1) / rows_per_tile;
+    int sum = cnt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+      const int up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
       if (lane >= o) sum += up;
     }
-    const int64_t all = __shfl_sync(0xFFFFFFFFu, sum, 31);
+    const int all = __shfl_sync(0xFFFFFFFFu, sum, 31);
     if (idx < before + all) {
       const unsigned hit = __ballot_sync(0xFFFFFFFFu, idx < before + sum);
       const int src = __ffs(static_cast<int>(hit)) - 1;
@@ -74,27 +84,28 @@ __device__ __forceinline__ PagedTile find_tile(const PagedAttnArgs& a, int rows_
       t.tok0 = __shfl_sync(0xFFFFFFFFu, lo, src);
       t.n = __shfl_sync(0xFFFFFFFFu, n, src);
       t.past = __shfl_sync(0xFFFFFFFFu, past, src);
-      const int64_t first = before + __shfl_sync(0xFFFFFFFFu, sum - cnt, src);
-      t.row0 = (idx - first) * rows_per_tile;
+      t.row0 = (idx - before - __shfl_sync(0xFFFFFFFFu, sum - cnt, src)) * rows_per_tile;
       return t;
     }
     before += all;
   }
-  PagedTile none;
-  none.req = -1;
-  none.tok0 = none.n = none.past = none.row0 = 0;
-  return none;
+  return PagedTile{-1, 0, 0, 0, 0};
 }
 
 // Page that holds row j of request b, or -1 (reported) when it is out of range.
-__device__ __forceinline__ int64_t page_of(const PagedAttnArgs& a, int b, int64_t j) {
-  const int64_t blk = j / a.kv.page_size;
+__device__ __forceinline__ int64_t page_of(const PagedAttnArgs& a, int b, int j) {
+  const int blk = j >> a.kv.page_shift;
   if (blk < a.kv.table_stride) {
     const int64_t page = __ldg(a.kv.table + static_cast<int64_t>(b) * a.kv.table_stride + blk);
     if (page >= 0 && page < a.kv.n_pages) return page;
   }
   report_error(a.err, kErrIndexRange);
   return -1;
+}
+
+// Row of j in its page.
+__device__ __forceinline__ int row_in_page(const PagedAttnArgs& a, int j) {
+  return j & (a.kv.page_size - 1);
 }
 
 }  // namespace tg
