@@ -32,7 +32,7 @@
 // (the chunk's own tokens, keys removed by their bias) are cleared, noted, and
 // added at the end to the rows that do see them.
 #include <algorithm>
-#include <atomic>
+#include <type_traits>
 
 #include "tg_device.cuh"
 #include "tg_internal.h"
@@ -44,20 +44,16 @@ namespace {
 constexpr int kBlk = 128;          // rows of a warpgroup = keys of a tile
 constexpr int kThreads = 384;
 constexpr int kSub = 128 * 128;    // [128 rows x 64 bf16], 128-byte swizzle
-constexpr int kAugTile = 128 * 32; // [128 rows x 16 bf16], 32-byte swizzle
 constexpr float kRescale = 8.0f;   // log2 units
-// Register split (setmaxnreg), as in k_attn_tc.cu: it must use exactly the
-// registers the CTA launched with; the launcher checks the compiled count.
-constexpr uint32_t kRegsLaunch = 168, kRegsLow = 72, kRegsHigh = 216;
-static_assert(kRegsLow * 128 + kRegsHigh * 256 == kRegsLaunch * kThreads, "register split");
 
 template <int kDh>
 struct Lay {
   static constexpr int kSubs = kDh / 64;
   static constexpr int kTile = kSubs * kSub;         // [128 x kDh] bf16
-  static constexpr int kOffQAug = 0;                 // A, B
-  static constexpr int kOffKAug = 2 * kAugTile;      // 4 stages
-  static constexpr int kOffQ = 6 * kAugTile;         // A, B
+  // the gate-bias K-steps: one tile whose four 16-column groups are the two
+  // stages of the keys and the rows of A and of B
+  static constexpr int kOffAug = 0;
+  static constexpr int kOffQ = kSub;                 // A, B
   static constexpr int kOffK = kOffQ + 2 * kTile;    // 2 stages
   static constexpr int kOffV = kOffK + 2 * kTile;    // 2 stages
   static constexpr int kOffBias = kOffV + 2 * kTile; // 4 x 128 fp32
@@ -113,11 +109,13 @@ __device__ __forceinline__ void split3(float x, float& p0, float& p1, float& p2)
   p1 = __bfloat162float(__float2bfloat16_rn(x - p0));
   p2 = x - p0 - p1;
 }
-// Row r of a 32-byte-swizzled [128 x 16] tile: 16-byte unit c sits at c ^ (r >> 2 & 1).
-__device__ __forceinline__ void store_aug(uint8_t* tile, int r, uint32_t a, uint32_t b, uint32_t c) {
-  const int sw = (r >> 2) & 1;
-  *reinterpret_cast<uint4*>(tile + r * 32 + (sw << 4)) = make_uint4(a, b, c, 0u);
-  *reinterpret_cast<uint4*>(tile + r * 32 + ((1 ^ sw) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+// Row r of 16-column group `col` of a 128-byte-swizzled tile. (In tiles of
+// their own with the 32-byte swizzle these K-steps took as long as half a
+// product: 587 us for 2048 tokens after 30720 where none takes 486.)
+__device__ __forceinline__ void store_aug(uint8_t* tile, int r, int col, uint32_t a, uint32_t b, uint32_t c) {
+  const int u = 2 * col, sw = r & 7;
+  *reinterpret_cast<uint4*>(tile + r * 128 + ((u ^ sw) << 4)) = make_uint4(a, b, c, 0u);
+  *reinterpret_cast<uint4*>(tile + r * 128 + (((u + 1) ^ sw) << 4)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // Clears the infinities and NaN among 8 bf16 values.
@@ -155,11 +153,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_ready = bars + 7;   // [2] and cleaned
   uint64_t* v_empty = bars + 9;   // [2]
   uint64_t* s_full = bars + 11;   // [A, B]
-  uint64_t* p_full = bars + 13;   // [A, B]
-  uint64_t* o_full = bars + 15;   // [A, B]
-  uint64_t* b_full = bars + 17;   // [4] biases and mask of a tile
-  uint64_t* b_empty = bars + 21;  // [4]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 25);
+  uint64_t* p_full = bars + 13;   // [A, B][halves of the keys]
+  uint64_t* o_full = bars + 17;   // [A, B]
+  uint64_t* b_full = bars + 19;   // [4] biases and mask of a tile
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 23);
   __shared__ PagedTile s_tile;
   __shared__ int s_found;
   __shared__ float2 s_ml[kBlk];
@@ -180,12 +177,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&v_ready[i], 1);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
       mbar_init(&o_full[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
+      mbar_init(&p_full[i], 4);  // the warps of a warpgroup
       mbar_init(&b_full[i], 1);
-      mbar_init(&b_empty[i], 1);
     }
     fence_mbar_init();
     tma_prefetch_desc(&tmK);
@@ -238,7 +234,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_h[2] = {dual ? (nt + 1) / 2 : nt, dual ? nt / 2 : nt};
 
   if (warp < 4) {
-    setmaxnreg_dec<kRegsLow>();
     if (warp == 0) {
       // ------------------------------------------------------------ TMA
       const int page = a.kv.page_size;
@@ -273,111 +268,123 @@ __global__ void __launch_bounds__(kThreads, 1)
         pg = pg1;
         pg1 = pg2;
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // ------------------------------------------------------------ MMA
+      // The whole warp runs this, on values it knows to be the same in every
+      // lane (a vote, a reduction), so that descriptors are formed and held in
+      // uniform registers.
+      const bool both = __any_sync(0xFFFFFFFFu, dual);
+      const int last_a = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(n_h[0])));
+      const int last_b = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(n_h[1])));
+      const uint32_t base = smem_addr(smem);
+      const uint32_t tm = __reduce_max_sync(0xFFFFFFFFu, tmem);
       auto qk = [&](int h, int t) {
         constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
-        const uint32_t q_addr = smem_addr(smem + L::kOffQ + (h && !dual ? L::kTile : 0));
-        const uint32_t k_addr = smem_addr(smem + L::kOffK + (t & 1) * L::kTile);
-        const uint32_t d = tmem + static_cast<uint32_t>(h * 128);
+        const uint64_t qd = sdesc_kmajor_sw128(base + L::kOffQ + (h && !both ? L::kTile : 0));
+        const uint64_t kd = sdesc_kmajor_sw128(base + L::kOffK + (t & 1) * L::kTile);
+        const uint32_t d = tm + static_cast<uint32_t>(h * 128);
 #pragma unroll
         for (int kk = 0; kk < kDh / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kSub + (kk & 3) * 32;
-          umma_f16_ss(d, sdesc_kmajor_sw128(q_addr + off), sdesc_kmajor_sw128(k_addr + off), idesc,
-                      kk > 0 ? 1u : 0u);
+          const uint32_t off = ((kk >> 2) * kSub + (kk & 3) * 32) >> 4;
+          umma_f16_ss_warp(d, qd + off, kd + off, idesc, kk > 0 ? 1u : 0u);
         }
         if (kBias)
-          umma_f16_ss(d, sdesc_kmajor_sw32(smem_addr(smem + L::kOffQAug + (h && !dual ? kAugTile : 0))),
-                      sdesc_kmajor_sw32(smem_addr(smem + L::kOffKAug + (t & 3) * kAugTile)), idesc, 1u);
-        umma_commit(&s_full[h]);
-        if (h == 1 || dual) umma_commit(&k_empty[t & 1]);
+          umma_f16_ss_warp(d, sdesc_kmajor_sw128(base + L::kOffAug + (h && !both ? 96 : 64)),
+                           sdesc_kmajor_sw128(base + L::kOffAug + (t & 1) * 32), idesc, 1u);
+        umma_commit_warp(&s_full[h]);
+        if (h == 1 || both) umma_commit_warp(&k_empty[t & 1]);
       };
-      auto pv = [&](int h, int t, bool first) {
+      auto pv = [&](int h, int t, int half, bool first) {
         constexpr uint32_t idesc = idesc_bmn(128, kDh);
-        const uint32_t v_addr = smem_addr(smem + L::kOffV + (t & 1) * L::kTile);
-        const uint32_t p_tm = tmem + static_cast<uint32_t>(h * 128);
-        const uint32_t d = tmem + 256u + static_cast<uint32_t>(h * 128);
+        const uint64_t vd = sdesc_mn(base + L::kOffV + (t & 1) * L::kTile, kSub);
+        const uint32_t p_tm = tm + static_cast<uint32_t>(h * 128);
+        const uint32_t d = tm + 256u + static_cast<uint32_t>(h * 128);
 #pragma unroll
-        for (int kk = 0; kk < kBlk / 16; ++kk)
-          umma_f16_ts(d, p_tm + static_cast<uint32_t>(kk * 8), sdesc_mn(v_addr + kk * 2048, kSub), idesc,
-                      (!first || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < 4; ++kk) {
+          const int ks = half * 4 + kk;
+          umma_f16_ts_warp(d, p_tm + static_cast<uint32_t>(ks * 8), vd + ((ks * 2048) >> 4), idesc,
+                           (!first || ks > 0) ? 1u : 0u);
+        }
       };
       auto k_there = [&](int t) -> bool {
-        return mbar_wait(&k_full[t & 1], (t >> 1) & 1, a.err) &&
-               (!kBias || mbar_wait(&b_full[t & 3], (t >> 2) & 1, a.err));
+        return mbar_wait_warp(&k_full[t & 1], (t >> 1) & 1, a.err) &&
+               (!kBias || mbar_wait_warp(&b_full[t & 3], (t >> 2) & 1, a.err));
       };
-      bool ok = mbar_wait(q_full, 0, a.err) && k_there(0);
+      bool ok = mbar_wait_warp(q_full, 0, a.err) && k_there(0);
       if (ok) {
         tc_fence_after();
         qk(0, 0);
-        if (n_h[1] > 0) {
-          if (dual) ok = k_there(1);
+        if (last_b > 0) {
+          if (both) ok = k_there(1);
           tc_fence_after();
-          if (ok) qk(1, dual ? 1 : 0);
+          if (ok) qk(1, both ? 1 : 0);
         }
       }
-      for (int j = 0; j < n_h[0] && ok; ++j) {
-#pragma unroll 1
-        for (int h = 0; h < 2 && ok; ++h) {
-          if (j >= n_h[h]) break;
-          const int t = dual ? 2 * j + h : j;
-          if (h == 0 || dual) ok = mbar_wait(&v_ready[t & 1], (t >> 1) & 1, a.err);
-          ok = ok && mbar_wait(&p_full[h], j & 1, a.err);
-          if (!ok) break;
+      // warpgroup h's step j
+      auto step = [&](auto hc, int j) -> bool {
+        constexpr int h = decltype(hc)::value;
+        const int n = h == 0 ? last_a : last_b;
+        const int t = both ? 2 * j + h : j;
+        if ((h == 0 || both) && !mbar_wait_warp(&v_ready[t & 1], (t >> 1) & 1, a.err)) return false;
+        // the next keys are there by now: P V and the next S go out back to back
+        const bool more = j + 1 < n;
+        const int tk = both ? t + 2 : j + 1;
+        if (more && (h == 0 || both) && !k_there(tk)) return false;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (!mbar_wait_warp(&p_full[2 * h + half], j & 1, a.err)) return false;
           tc_fence_after();
-          pv(h, t, j == 0);
-          if (j + 1 == n_h[h]) umma_commit(&o_full[h]);
-          if (h == 1 || dual) {
-            umma_commit(&v_empty[t & 1]);
-            if (kBias) umma_commit(&b_empty[t & 3]);  // both softmaxes have read the mask
-          }
-          if (j + 1 < n_h[h]) {
-            const int tk = dual ? t + 2 : j + 1;
-            if (h == 0 || dual) ok = k_there(tk);
-            if (!ok) break;
-            tc_fence_after();
-            qk(h, tk);
-          }
+          pv(h, t, half, j == 0);
         }
+        if (more) qk(h, tk);
+        else umma_commit_warp(&o_full[h]);
+        if (h == 1 || both) umma_commit_warp(&v_empty[t & 1]);
+        return true;
+      };
+      for (int j = 0; j < last_a && ok; ++j) {
+        ok = step(std::integral_constant<int, 0>(), j);
+        if (ok && j < last_b) ok = step(std::integral_constant<int, 1>(), j);
       }
     } else if (warp == 2 && kBias) {
       // ------------------------------------------------------------ gate biases
-      // four keys a lane: lane, lane + 32, ...; pages two tiles ahead, biases one
-      auto page_at = [&](int t, int i) -> int64_t {
-        const int j = lo + t * kBlk + lane + 32 * i;
-        return t < nt && j < hi ? page_of(a, tile.req, j) : -1;
+      // Keys lane, lane + 32, ... of a tile (rows of their K-step that store
+      // without bank conflicts). Lane l holds the page of keys 16 (l & 7) on; pages
+      // two tiles ahead, biases one.
+      auto page_at = [&](int t) -> int {
+        const int j = lo + t * kBlk + (lane & 7) * 16;
+        return t < nt && j < hi ? static_cast<int>(page_of(a, tile.req, j)) : -1;
       };
-      auto bias_at = [&](int t, int i, int64_t p) -> float {
-        if (p < 0) return 0.f;
-        return __ldg(a.kv.bias + p * a.kv.bias_page_stride + row_in_page(a, lo + t * kBlk + lane + 32 * i));
+      auto bias_at = [&](int t, int pages, float (&b)[4]) {
+        const int j = lo + t * kBlk + lane;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t p = __shfl_sync(0xFFFFFFFFu, pages, (lane >> 4) + 2 * i);
+          b[i] = p >= 0 && j + 32 * i < hi
+                     ? __ldg(a.kv.bias + p * a.kv.bias_page_stride + row_in_page(a, j + 32 * i))
+                     : 0.f;
+        }
       };
       float b[4];
-      int64_t pg[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        b[i] = bias_at(0, i, page_at(0, i));
-        pg[i] = page_at(1, i);
-      }
+      bias_at(0, page_at(0), b);
+      int pg = page_at(1);
+#pragma unroll 1
       for (int t = 0; t < nt; ++t) {
         float nb[4];
+        bias_at(t + 1, pg, nb);
+        pg = page_at(t + 2);
+        // QK(t - 2) has read its K-step; so the softmax of tile t - 4 is over
+        if (!mbar_wait_warp(&k_empty[t & 1], ((t >> 1) & 1) ^ 1, a.err)) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          nb[i] = bias_at(t + 1, i, pg[i]);
-          pg[i] = page_at(t + 2, i);
-        }
-        if (!mbar_wait_warp(&b_empty[t & 3], ((t >> 2) & 1) ^ 1, a.err)) break;
-        uint8_t* tile_aug = smem + L::kOffKAug + (t & 3) * kAugTile;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = lane + 32 * i;
           const bool rem = b[i] < kRemovableBias;
           const unsigned bits = __ballot_sync(0xFFFFFFFFu, rem);
           if (lane == 0) s_mask[(t & 3) * 4 + i] = bits;
-          s_bias[(t & 3) * 128 + r] = key_bias(b[i]);
+          s_bias[(t & 3) * 128 + lane + 32 * i] = key_bias(b[i]);
           float b0, b1, b2;
           split3(rem ? 0.f : b[i], b0, b1, b2);
           // against (g0, g0, g1, g0, g2, g1)
-          store_aug(tile_aug, r, pack_bf16x2(b0, b1), pack_bf16x2(b0, b2), pack_bf16x2(b0, b1));
+          store_aug(smem + L::kOffAug, lane + 32 * i, t & 1, pack_bf16x2(b0, b1), pack_bf16x2(b0, b2),
+                    pack_bf16x2(b0, b1));
           b[i] = nb[i];
         }
         fence_async_smem();
@@ -421,7 +428,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    setmaxnreg_inc<kRegsHigh>();
     // -------------------------------------------------------------- softmax
     const int h = (warp - 4) >> 2;            // warpgroup A or B
     const int r = (threadIdx.x - 128) & 127;  // row of the warpgroup = TMEM lane
@@ -453,8 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kBias) {
         float g0, g1, g2;
         split3(gain * sqrtf(static_cast<float>(kDh)) * tau, g0, g1, g2);
-        store_aug(smem + L::kOffQAug + (dual ? 0 : h * kAugTile), r, pack_bf16x2(g0, g0),
-                  pack_bf16x2(g1, g0), pack_bf16x2(g2, g1));
+        store_aug(smem + L::kOffAug, r, 2 + (dual ? 0 : h), pack_bf16x2(g0, g0), pack_bf16x2(g1, g0),
+                  pack_bf16x2(g2, g1));
       }
       fence_async_smem();
     }
@@ -498,73 +504,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st32_wait(s_tm + static_cast<uint32_t>(c * 32), z);
         }
       }
-      float x[128];
-      {
-        uint32_t r0[32], r1[32], r2[32], r3[32];
-        tmem_ld32(s_tm, r0);
-        tmem_ld32(s_tm + 32, r1);
-        tmem_ld32(s_tm + 64, r2);
-        tmem_ld32(s_tm + 96, r3);
-        tmem_wait_ld_dep(r3);
-        tmem_ld_fence(r0);
-        tmem_ld_fence(r1);
-        tmem_ld_fence(r2);
+      // The row's maximum, 64 logits at a time.
+      float mx = -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 64) {
+        uint32_t u0[32], u1[32];
+        tmem_ld32(s_tm + static_cast<uint32_t>(c), u0);
+        tmem_ld32(s_tm + static_cast<uint32_t>(c + 32), u1);
+        tmem_wait_ld_dep(u1);
+        tmem_ld_fence(u0);
+        float mx4[4];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          x[i] = __uint_as_float(r0[i]);
-          x[32 + i] = __uint_as_float(r1[i]);
-          x[64 + i] = __uint_as_float(r2[i]);
-          x[96 + i] = __uint_as_float(r3[i]);
-        }
+        for (int k = 0; k < 4; ++k)
+          mx4[k] = fmax3f(__uint_as_float(u0[k]), __uint_as_float(u0[4 + k]), __uint_as_float(u1[k]));
+#pragma unroll
+        for (int i = 8; i < 32; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx4[k] = fmax3f(mx4[k], __uint_as_float(u0[i + k]), __uint_as_float(u0[i + 4 + k]));
+#pragma unroll
+        for (int i = 4; i < 28; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx4[k] = fmax3f(mx4[k], __uint_as_float(u1[i + k]), __uint_as_float(u1[i + 4 + k]));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx4[k] = fmaxf(mx4[k], __uint_as_float(u1[28 + k]));
+        mx = fmax3f(mx, fmax3f(mx4[0], mx4[1], mx4[2]), mx4[3]);
       }
-      // eight chains of 3-input maxima
-      float mx8[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) mx8[k] = fmax3f(x[k], x[8 + k], x[16 + k]);
-#pragma unroll
-      for (int i = 24; i < 120; i += 16)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mx8[k] = fmax3f(mx8[k], x[i + k], x[i + 8 + k]);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(mx8[k], x[120 + k]);
-      const float mx = fmax3f(fmax3f(mx8[0], mx8[1], mx8[2]), fmax3f(mx8[3], mx8[4], mx8[5]),
-                              fmaxf(mx8[6], mx8[7])) *
-                       scale2;
+      mx *= scale2;
       float alpha = 1.0f;
       if (mx > m + kRescale || (m == -INFINITY && mx != -INFINITY)) {
         alpha = ex2_approx(m - mx);  // 0 on the first keys
         l *= alpha;
         m = mx;
       }
-      const bool rescale_o = j > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.0f);
-      // P = 2^(S scale2 - m) in packed pairs, one pair in four on the FMA pipe
-      // (the MUFU unit is this loop's bottleneck)
-      const float base = m == -INFINITY ? 0.f : m;
-      float2 sp[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                      make_float2(0.f, 0.f)};
-      const float2 sc2 = make_float2(scale2, scale2), nm2 = make_float2(-base, -base);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float2 y = ffma2(make_float2(x[64 * half + 2 * i], x[64 * half + 2 * i + 1]), sc2, nm2);
-          float2 e;
-          if ((i & 3) == 3) {
-            e = exp2_fma(y);
-          } else {
-            e.x = ex2_approx(y.x);
-            e.y = ex2_approx(y.y);
-          }
-          sp[i & 3] = fadd2(sp[i & 3], e);
-          pk[i] = pack_bf16x2(e.x, e.y);
-        }
-        tmem_st32(s_tm + static_cast<uint32_t>(32 * half), pk);
-        tmem_wait_st();
-      }
-      const float2 s2 = fadd2(fadd2(sp[0], sp[1]), fadd2(sp[2], sp[3]));
-      l += s2.x + s2.y;
-      if (rescale_o) {
+      if (j > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
 #pragma unroll 1
         for (int c = 0; c < kDh / 32; ++c) {
           float o[32];
@@ -575,8 +549,52 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st32_wait(ta, o);
         }
       }
-      tc_fence_before();
-      mbar_arrive(&p_full[h]);
+      // P = 2^(S scale2 - m), 32 keys at a time (read again from TMEM: held in
+      // registers from the maximum on, the 128 logits unroll this loop to a
+      // size that the instruction cache does not hold beside the other warps'
+      // code), in packed pairs, one pair in four on the FMA pipe (the MUFU unit
+      // is this loop's bottleneck). 32 keys' P covers 16 columns of logits that
+      // have been read.
+      const float base = m == -INFINITY ? 0.f : m;
+      float2 sp[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                      make_float2(0.f, 0.f)};
+      const float2 sc2 = make_float2(scale2, scale2), nm2 = make_float2(-base, -base);
+      uint32_t y0[32], y1[32];
+      auto weights = [&](uint32_t (&u)[32], int c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 y =
+              ffma2(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), sc2, nm2);
+          float2 e;
+          if ((i & 3) == 3) {
+            e = exp2_fma(y);
+          } else {
+            e.x = ex2_approx(y.x);
+            e.y = ex2_approx(y.y);
+          }
+          sp[i & 3] = fadd2(sp[i & 3], e);
+          pk[i] = pack_bf16x2(e.x, e.y);
+        }
+        tmem_st16(s_tm + static_cast<uint32_t>(16 * c), pk);
+      };
+      tmem_ld32(s_tm, y0);
+      tmem_wait_ld_dep(y0);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        tmem_ld32(s_tm + static_cast<uint32_t>(64 * half + 32), y1);
+        weights(y0, 2 * half);
+        tmem_wait_ld_dep(y1);
+        if (half == 0) tmem_ld32(s_tm + 64u, y0);
+        weights(y1, 2 * half + 1);
+        tmem_wait_ld_dep(y0);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * h + half]);  // P V of these keys may start
+      }
+      const float2 s2 = fadd2(fadd2(sp[0], sp[1]), fadd2(sp[2], sp[3]));
+      l += s2.x + s2.y;
     }
     // -------------------------------------------------------------- output
     // With `dual`, B's rows wait in the idle K tiles for A's threads.
@@ -738,14 +756,6 @@ cudaError_t run(const PagedAttnArgs& a, cudaStream_t st) {
     return cudaErrorInvalidValue;
   auto kern = paged_attn_tc<kDh, kBias>;
   TG_CUDA_TRY(set_smem_attr_once(reinterpret_cast<const void*>(kern), static_cast<int>(L::kSmem)));
-  // With any other register count setmaxnreg.inc could block: refuse.
-  static std::atomic<int> regs_ok{0};
-  if (regs_ok.load() == 0) {
-    cudaFuncAttributes fa;
-    TG_CUDA_TRY(cudaFuncGetAttributes(&fa, reinterpret_cast<const void*>(kern)));
-    regs_ok.store(fa.numRegs == int(kRegsLaunch) ? 1 : -1);
-  }
-  if (regs_ok.load() < 0) return cudaErrorInvalidConfiguration;
   const int64_t grid = a.tiles * a.splits * a.kv.hkv;
   return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), L::kSmem, st, tk, tv, a);
 }
