@@ -12,6 +12,7 @@ it raises ImportError -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Dict, List, Optional, Sequence
@@ -666,26 +667,33 @@ def tg_prefill_batch(model: Model, x, protect, lens: Sequence[int], ks: Sequence
 
 
 # ----------------------------------------------------------------- paged cache
+#
+# These calls are made once a layer and token, where the kernel takes a few
+# microseconds: their checks form no message unless they fail.
+
+_cur_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
+_cur_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-class _on:
-    """Makes `device` the current one for a call (nothing to do when it is)."""
+def _stream_at(stream, index: int):
+    """_stream for the device `index`."""
+    if stream is None:
+        if _cur_stream is not None:
+            return _cur_stream(index)
+        return torch.cuda.current_stream(index).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
-    __slots__ = ("dev", "prev")
 
-    def __init__(self, device):
-        _need(device.type == "cuda", "tensors must be on a CUDA device")
-        self.dev = device.index
-
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        self.prev = None if cur == self.dev else cur
-        if self.prev is not None:
-            torch.cuda.set_device(self.dev)
-
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            torch.cuda.set_device(self.prev)
+def _call(index: int, fn, name: str, *args) -> None:
+    """fn(*args) with device `index` as the current one."""
+    cur = _cur_device() if _cur_device is not None else torch.cuda.current_device()
+    if cur == index:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args)
+    if status != TG_OK:
+        raise TokenGateError(status, name)
 
 
 def _need(cond: bool, what: str) -> None:
@@ -693,24 +701,38 @@ def _need(cond: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _vec(t, n: int, dtype, device, name: str):
+def _device_index(t: torch.Tensor) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    return index
+
+
+def _vec(t, n: int, dtype, index: int, name: str):
     """Pointer of an optional contiguous 1-D tensor of n elements."""
     if t is None:
         return None
-    _need(t.dtype == dtype and t.device == device and t.numel() == n and t.is_contiguous(),
-          f"{name} must be a contiguous {dtype} tensor of {n} elements on {device}")
+    if t.dtype is not dtype or t.get_device() != index or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on cuda:{index}")
     return t.data_ptr()
 
 
-def _rows3(t, rows: int, heads: int, dh: int, dtype, device, name: str) -> int:
+def _rows3(t, rows: int, heads: int, dh: int, dtype, index: int, name: str) -> int:
     """Row stride of a [rows, heads, dh] tensor whose rows are contiguous."""
-    _need(t.dtype == dtype and t.device == device and t.shape == (rows, heads, dh),
-          f"{name} must be {dtype} [{rows}, {heads}, {dh}] on {device}")
+    if t.dtype is not dtype or t.get_device() != index or t.shape != (rows, heads, dh):
+        raise ValueError(f"{name} must be {dtype} [{rows}, {heads}, {dh}] on cuda:{index}")
     if rows == 0:
         return heads * dh
     s0, s1, s2 = t.stride()
-    _need(s2 == 1 and (heads == 1 or s1 == dh), f"{name}: each row must be contiguous")
+    if s2 != 1 or (s1 != dh and heads != 1):
+        raise ValueError(f"{name}: each row must be contiguous")
     return s0 if rows > 1 else max(s0, heads * dh)
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_ws_bytes(batch: int, rows: int, hq: int, hkv: int, dh: int, dtype: int) -> int:
+    return tg_workspace_size(TG_OP_PAGED_ATTN, n=batch, k=rows, n_heads_q=hq, n_heads_kv=hkv,
+                             head_dim=dh, dtype=dtype)
 
 
 class PagedKV:
@@ -736,6 +758,8 @@ class PagedKV:
         self.k, self.v, self.table, self.bias = k, v, table, bias
         self.page_size, self.n_heads_kv, self.head_dim = ps, hkv, dh
         self.dtype, self.device = k.dtype, k.device
+        self.batch = table.shape[0]
+        self.capacity = table.shape[1] * ps  # rows that the table has room for, per request
         page = ps * hkv * dh
 
         def apart(t, least):
@@ -746,15 +770,7 @@ class PagedKV:
                            0 if bias is None else apart(bias, ps), table.shape[1], ps, hkv, dh,
                            _dt(k))
         self._ref = ctypes.byref(self.c)
-
-    @property
-    def batch(self) -> int:
-        return self.table.shape[0]
-
-    @property
-    def capacity(self) -> int:
-        """Rows that the table has room for, per request."""
-        return self.table.shape[1] * self.page_size
+        self._index, self._tg_dtype = k.get_device(), self.c.dtype
 
 
 def tg_paged_append(cache: PagedKV, k, v, cu_q, kv_len, q=None, pos=None, s=None, q_norm=None,
@@ -767,31 +783,30 @@ def tg_paged_append(cache: PagedKV, k, v, cu_q, kv_len, q=None, pos=None, s=None
     None, all possibly slices of one fused projection; cu_q [batch + 1],
     kv_len [batch] (the new rows included) int32. Returns the rotated queries
     [rows, hq, dh], or None without q."""
-    dev, dt, dh = cache.device, cache.dtype, cache.head_dim
-    rows, nb = k.shape[0], cache.batch
-    k_st = _rows3(k, rows, cache.n_heads_kv, dh, dt, dev, "k")
-    v_st = _rows3(v, rows, cache.n_heads_kv, dh, dt, dev, "v")
+    index, dt, dh, nb = _device_index(cache.k), cache.dtype, cache.head_dim, cache.batch
+    hkv, rows = cache.n_heads_kv, k.shape[0]
+    k_st = _rows3(k, rows, hkv, dh, dt, index, "k")
+    v_st = _rows3(v, rows, hkv, dh, dt, index, "v")
     hq = q_st = 0
+    q_ptr = out_ptr = None
     if q is not None:
         hq = q.shape[1]
-        q_st = _rows3(q, rows, hq, dh, dt, dev, "q")
+        q_st = _rows3(q, rows, hq, dh, dt, index, "q")
         if q_out is None:
-            q_out = torch.empty((rows, hq, dh), dtype=dt, device=dev)
-        else:
-            _need(q_out.shape == (rows, hq, dh) and q_out.dtype == dt and q_out.device == dev
-                  and q_out.is_contiguous(), "q_out must be contiguous, as q in shape and dtype")
-    else:
-        _need(q_out is None, "q_out without q")
-    f32 = torch.float32
-    with _on(dev):
-        _check(_paged_append(
-            cache._ref, None if q is None else q.data_ptr(), q_st, k.data_ptr(), k_st,
-            v.data_ptr(), v_st, rows, _vec(cu_q, nb + 1, torch.int32, dev, "cu_q"),
-            _vec(kv_len, nb, torch.int32, dev, "kv_len"), nb, hq,
-            _vec(pos, rows, torch.int32, dev, "pos"), _vec(s, rows, f32, dev, "s"),
-            _vec(q_norm, dh, f32, dev, "q_norm"), _vec(k_norm, dh, f32, dev, "k_norm"), eps,
-            rope_base, None if q_out is None else q_out.data_ptr(), _stream(stream, dev)),
-            "tg_paged_append")
+            q_out = torch.empty((rows, hq, dh), dtype=dt, device=cache.device)
+        elif (q_out.shape != (rows, hq, dh) or q_out.dtype is not dt or q_out.get_device() != index
+              or not q_out.is_contiguous()):
+            raise ValueError("q_out must be contiguous, as q in shape and dtype")
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    i32, f32 = torch.int32, torch.float32
+    _call(index, _paged_append, "tg_paged_append", cache._ref, q_ptr, q_st, k.data_ptr(), k_st,
+          v.data_ptr(), v_st, rows, _vec(cu_q, nb + 1, i32, index, "cu_q"),
+          _vec(kv_len, nb, i32, index, "kv_len"), nb, hq, _vec(pos, rows, i32, index, "pos"),
+          _vec(s, rows, f32, index, "s"), _vec(q_norm, dh, f32, index, "q_norm"),
+          _vec(k_norm, dh, f32, index, "k_norm"), eps, rope_base, out_ptr,
+          _stream_at(stream, index))
     return q_out
 
 
@@ -802,26 +817,25 @@ def tg_paged_attn(cache: PagedKV, q, cu_q, kv_len, gain=None, tau=None,
     dh] rotated; gain, tau [hq] fp32; max_kv: an upper bound of kv_len (None:
     the table's capacity). lse [hq, rows] fp32 is written when given. Returns
     out [rows, hq, dh]."""
-    dev, dt, dh = cache.device, cache.dtype, cache.head_dim
-    rows, hq, nb = q.shape[0], q.shape[1], cache.batch
-    q_st = _rows3(q, rows, hq, dh, dt, dev, "q")
+    index, dt, dh, nb = _device_index(cache.k), cache.dtype, cache.head_dim, cache.batch
+    rows, hq = q.shape[0], q.shape[1]
+    q_st = _rows3(q, rows, hq, dh, dt, index, "q")
     if out is None:
-        out = torch.empty((rows, hq, dh), dtype=dt, device=dev)
-    else:
-        _need(out.shape == (rows, hq, dh) and out.dtype == dt and out.device == dev
-              and out.is_contiguous(), "out must be contiguous, as q in shape and dtype")
-    need = tg_workspace_size(TG_OP_PAGED_ATTN, n=nb, k=rows, n_heads_q=hq,
-                             n_heads_kv=cache.n_heads_kv, head_dim=dh, dtype=cache.c.dtype)
-    ws = _ws(need, dev, ws)
-    f32 = torch.float32
-    with _on(dev):
-        _check(_paged_attn(
-            cache._ref, q.data_ptr(), q_st, rows, _vec(cu_q, nb + 1, torch.int32, dev, "cu_q"),
-            _vec(kv_len, nb, torch.int32, dev, "kv_len"), nb, hq,
-            cache.capacity if max_kv is None else int(max_kv), _vec(gain, hq, f32, dev, "gain"),
-            _vec(tau, hq, f32, dev, "tau"), out.data_ptr(), _vec(lse, hq * rows, f32, dev, "lse"),
-            ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream, dev)),
-            "tg_paged_attn")
+        out = torch.empty((rows, hq, dh), dtype=dt, device=cache.device)
+    elif (out.shape != (rows, hq, dh) or out.dtype is not dt or out.get_device() != index
+          or not out.is_contiguous()):
+        raise ValueError("out must be contiguous, as q in shape and dtype")
+    need = _paged_ws_bytes(nb, rows, hq, cache.n_heads_kv, dh, cache._tg_dtype)
+    ws_ptr, ws_bytes = None, 0
+    if need > 0 or ws is not None:
+        ws = _ws(need, cache.device, ws)
+        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    i32, f32 = torch.int32, torch.float32
+    _call(index, _paged_attn, "tg_paged_attn", cache._ref, q.data_ptr(), q_st, rows,
+          _vec(cu_q, nb + 1, i32, index, "cu_q"), _vec(kv_len, nb, i32, index, "kv_len"), nb, hq,
+          cache.capacity if max_kv is None else int(max_kv), _vec(gain, hq, f32, index, "gain"),
+          _vec(tau, hq, f32, index, "tau"), out.data_ptr(), _vec(lse, hq * rows, f32, index, "lse"),
+          ws_ptr, ws_bytes, _stream_at(stream, index))
     return out
 
 
@@ -832,19 +846,20 @@ def tg_quantize_rows(x, xq=None, scale=None, stream=None):
     """Rows of x [rows, cols] (bf16 or fp32, cols % 16 == 0) as 8-bit integers
     with one scale each: (xq [rows, cols] int8, scale [rows] fp32)."""
     rows, cols = x.shape
-    dev = x.device
-    _need(rows == 0 or cols <= 1 or x.stride(1) == 1, "x: each row must be contiguous")
+    index = _device_index(x)
+    x_st, step = x.stride()
+    if step != 1 and rows > 0 and cols > 1:
+        raise ValueError("x: each row must be contiguous")
     if xq is None:
-        xq = torch.empty((rows, cols), dtype=torch.int8, device=dev)
-    else:
-        _need(xq.shape == x.shape and xq.dtype == torch.int8 and xq.device == dev
-              and xq.is_contiguous(), "xq must be contiguous int8 of x's shape")
+        xq = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+    elif (xq.shape != x.shape or xq.dtype is not torch.int8 or xq.get_device() != index
+          or not xq.is_contiguous()):
+        raise ValueError("xq must be contiguous int8 of x's shape")
     if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=dev)
-    with _on(dev):
-        _check(_quantize(x.data_ptr(), x.stride(0) if rows > 1 else cols, rows, cols, _dt(x),
-                         xq.data_ptr(), _vec(scale, rows, torch.float32, dev, "scale"),
-                         _stream(stream, dev)), "tg_quantize_rows")
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _call(index, _quantize, "tg_quantize_rows", x.data_ptr(), x_st if rows > 1 else cols, rows, cols,
+          _dt(x), xq.data_ptr(), _vec(scale, rows, torch.float32, index, "scale"),
+          _stream_at(stream, index))
     return xq, scale
 
 
@@ -854,20 +869,25 @@ def tg_linear_quantized(xq, xs, wq, ws, residual=None, y=None, dtype=torch.bfloa
     residual [m, n] in dtype (bf16 or fp32)."""
     m, k = xq.shape
     n = wq.shape[0]
-    dev = xq.device
-    _need(wq.shape == (n, k) and xq.dtype == torch.int8 and wq.dtype == torch.int8
-          and wq.device == dev and xq.is_contiguous() and wq.is_contiguous(),
-          "xq [m, k] and wq [n, k] must be contiguous int8 on one device")
+    index = _device_index(xq)
+    i8 = torch.int8
+    if (wq.shape != (n, k) or xq.dtype is not i8 or wq.dtype is not i8 or wq.get_device() != index
+            or not xq.is_contiguous() or not wq.is_contiguous()):
+        raise ValueError("xq [m, k] and wq [n, k] must be contiguous int8 on one device")
     if y is None:
-        y = torch.empty((m, n), dtype=dtype, device=dev)
-    for name, t in (("y", y), ("residual", residual)):
-        _need(t is None or (t.shape == (m, n) and t.dtype == y.dtype and t.device == dev
-                            and t.is_contiguous()), f"{name} must be contiguous [m, n], as y")
-    with _on(dev):
-        _check(_linear_q(xq.data_ptr(), _vec(xs, m, torch.float32, dev, "xs"), wq.data_ptr(),
-                         _vec(ws, n, torch.float32, dev, "ws"),
-                         None if residual is None else residual.data_ptr(), m, n, k, _dt(y),
-                         y.data_ptr(), _stream(stream, dev)), "tg_linear_quantized")
+        y = torch.empty((m, n), dtype=dtype, device=xq.device)
+    elif y.shape != (m, n) or y.get_device() != index or not y.is_contiguous():
+        raise ValueError("y must be contiguous [m, n] on xq's device")
+    res_ptr = None
+    if residual is not None:
+        if (residual.shape != (m, n) or residual.dtype is not y.dtype
+                or residual.get_device() != index or not residual.is_contiguous()):
+            raise ValueError("residual must be contiguous [m, n], as y")
+        res_ptr = residual.data_ptr()
+    f32 = torch.float32
+    _call(index, _linear_q, "tg_linear_quantized", xq.data_ptr(), _vec(xs, m, f32, index, "xs"),
+          wq.data_ptr(), _vec(ws, n, f32, index, "ws"), res_ptr, m, n, k, _dt(y), y.data_ptr(),
+          _stream_at(stream, index))
     return y
 
 

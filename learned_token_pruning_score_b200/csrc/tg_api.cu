@@ -2010,8 +2010,17 @@ tg_status tg_paged_append(const tg_paged_kv* cache, const void* q, int64_t q_str
   a.eps = eps;
   a.rotate = rope_base > 0.f;
   a.q_out = q_out;
-  for (int i = 0; a.rotate && i < dh / 2; ++i)
-    a.theta[i] = std::exp2(-(2.0 * i / dh) * std::log2(static_cast<double>(rope_base)));
+  if (a.rotate) {
+    // the frequencies of the last base and head_dim (a process has one of each)
+    thread_local struct { float base = 0.f; int dh = 0; double theta[64]; } last;
+    if (last.base != rope_base || last.dh != dh) {
+      last.base = rope_base;
+      last.dh = dh;
+      for (int i = 0; i < dh / 2; ++i)
+        last.theta[i] = std::exp2(-(2.0 * i / dh) * std::log2(static_cast<double>(rope_base)));
+    }
+    std::copy(last.theta, last.theta + dh / 2, a.theta);
+  }
   a.err = device_error_word();
   const double bytes = 2.0 * rows * (hq + 2 * hkv) * dh * double(elem_size(dt));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
