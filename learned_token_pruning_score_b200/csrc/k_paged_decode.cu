@@ -33,6 +33,7 @@ constexpr int kKeys = 64;    // keys of a ring stage, 16 for each consumer warp
 constexpr int kThreads = 160;
 constexpr int kRing = 96 * 1024;  // two CTAs on an SM
 constexpr float kRescale = 8.0f;  // log2 units
+constexpr int kMaxCluster = 16;
 
 template <int kDh>
 struct Cfg {
@@ -41,7 +42,7 @@ struct Cfg {
   static constexpr int kStageBytes = 2 * kSubs * kSub;    // K, then V
   static constexpr int kStages = kRing / kStageBytes;
   static constexpr size_t kSmem = 1024 + kRing + 1024;    // (bias and barriers are static)
-  static_assert(4 * kRows * kDh * 4 <= kRing, "the warps' outputs reuse the ring");
+  static_assert(5 * kRows * kDh * 4 <= kRing, "the warps' outputs reuse the ring");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -81,7 +82,23 @@ __device__ __forceinline__ uint32_t clean_pair(uint32_t v, uint32_t dead, uint32
   return v;
 }
 
-template <int kDh>
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+// kCluster: the splits of a tile are the CTAs of a cluster and merge through
+// distributed shared memory.
+template <int kDh, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 2)
     paged_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const __grid_constant__ PagedAttnArgs a) {
@@ -93,10 +110,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ float s_m[4][kRows], s_l[4][kRows];
   __shared__ PagedTile s_tile;
   __shared__ int s_found;
+  __shared__ float2 s_out_ml[kRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.kv.hkv));
-  const int rest = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.kv.hkv));
-  const int split = rest % a.splits, tile_idx = rest / a.splits;
+  // heads innermost (a page's heads are read at the same time), or the splits
+  // where they have to be neighbours
+  const unsigned inner = static_cast<unsigned>(kCluster ? a.splits : a.kv.hkv);
+  const int b_in = static_cast<int>(blockIdx.x % inner), b_out = static_cast<int>(blockIdx.x / inner);
+  const int g = kCluster ? b_out % a.kv.hkv : b_in;
+  const int split = kCluster ? b_in : b_out % a.splits;
+  const int tile_idx = b_out / (kCluster ? a.kv.hkv : a.splits);
   const int group = a.hq / a.kv.hkv;
   pdl_trigger();
   if (threadIdx.x == 0) {
@@ -391,7 +413,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int rr = tile.row0 + r;
     const int64_t t = tile.tok0 + rr / group;
     const int h = g * group + rr % group;
-    if (a.splits > 1) {
+    if (kCluster) {
+      if (c == 0) s_out_ml[r] = make_float2(top, sum);
+      *reinterpret_cast<float4*>(acc + 4 * kRows * kDh + r * kDh + c) = v;
+    } else if (a.splits > 1) {
       const int64_t at = (split * a.rows + t) * a.hq + h;
       if (c == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(top, sum);
       if (blocks > 0) *reinterpret_cast<float4*>(a.part_o + at * kDh + c) = v;
@@ -403,6 +428,49 @@ __global__ void __launch_bounds__(kThreads, 2)
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (t * a.hq + h) * kDh + c) =
           make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
     }
+  }
+  if constexpr (kCluster) {
+    cluster_sync();
+    // row r is merged by CTA r % splits: the parts' states, in their order
+    for (int e = threadIdx.x; e < kRows * (kDh / 4); e += kThreads) {
+      const int r = e / (kDh / 4), c = (e % (kDh / 4)) * 4;
+      if (r >= n_rows) break;
+      if (r % a.splits != split) continue;
+      const uint32_t ml_at = smem_addr(&s_out_ml[r]), o_at = smem_addr(acc + 4 * kRows * kDh + r * kDh + c);
+      float2 ml[kMaxCluster];
+      float4 o4[kMaxCluster];
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {
+        ml[q] = make_float2(-INFINITY, 0.f);
+        o4[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (q < a.splits) {
+          ml[q] = ld_cluster2(mapa_shared(ml_at, static_cast<uint32_t>(q)));
+          o4[q] = ld_cluster(mapa_shared(o_at, static_cast<uint32_t>(q)));
+        }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) top = fmaxf(top, ml[q].x);
+      float sum = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {
+        const float w = state_weight(ml[q].x, ml[q].y, top);
+        sum = fmaf(ml[q].y, w, sum);
+        v = make_float4(fmaf(o4[q].x, w, v.x), fmaf(o4[q].y, w, v.y), fmaf(o4[q].z, w, v.z),
+                        fmaf(o4[q].w, w, v.w));
+      }
+      const int rr = tile.row0 + r;
+      const int64_t t = tile.tok0 + rr / group;
+      const int h = g * group + rr % group;
+      const bool any = sum != 0.f;
+      const float inv = any ? 1.0f / sum : 0.f;
+      if (c == 0 && a.lse != nullptr)
+        a.lse[h * a.rows + t] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (t * a.hq + h) * kDh + c) =
+          make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+    }
+    cluster_sync();  // the others have read this CTA's state
   }
 }
 
@@ -506,7 +574,7 @@ cudaError_t merge(const PagedAttnArgs& a, cudaStream_t st) {
 }
 
 template <int kDh>
-cudaError_t run(const PagedAttnArgs& a, int64_t tiles, cudaStream_t st) {
+cudaError_t run(const PagedAttnArgs& a, int64_t tiles, bool cluster, cudaStream_t st) {
   using C = Cfg<kDh>;
   CUtensorMap tk, tv;
   const int box = a.kv.page_size < kKeys ? a.kv.page_size : kKeys;
@@ -515,11 +583,28 @@ cudaError_t run(const PagedAttnArgs& a, int64_t tiles, cudaStream_t st) {
       !make_tmap_pages_bf16(&tv, a.kv.v, kDh, a.kv.hkv, a.kv.page_size, a.kv.n_pages,
                             a.kv.v_page_stride, box))
     return cudaErrorInvalidValue;
-  auto kern = paged_decode<kDh>;
-  TG_CUDA_TRY(set_smem_attr_once(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmem)));
   const int64_t grid = tiles * a.splits * a.kv.hkv;
-  TG_CUDA_TRY(launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), C::kSmem, st, tk, tv, a));
-  return cudaSuccess;
+  auto launch = [&](auto kern, int cluster) -> cudaError_t {
+    TG_CUDA_TRY(set_smem_attr_once(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmem)));
+    if (cluster > 8)
+      TG_CUDA_TRY(cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, tk, tv, a);
+  };
+  return cluster ? launch(paged_decode<kDh, true>, a.splits) : launch(paged_decode<kDh, false>, 1);
 }
 
 }  // namespace
@@ -531,6 +616,20 @@ cudaError_t launch_paged_merge(const PagedAttnArgs& a, cudaStream_t st) {
 cudaError_t launch_paged_decode(PagedAttnArgs a, void* ws, cudaStream_t st) {
   const int64_t tiles = paged_row_tiles(a.rows, a.batch, a.hq, a.kv.hkv, kRows);
   const int64_t jobs = tiles * a.kv.hkv;
+  // Few jobs over keys that 16 splits of 128 hold: a cluster for each, which
+  // merges its splits itself (one token, 8 KV heads: 1000 keys 8.8 us, 2000
+  // keys 9.2; merged by a second kernel 11.0 and 10.0. Over 4096 keys, 16
+  // splits no longer draw on enough SMs: 15.4 against 13.5).
+  int cluster = kMaxCluster;
+  while (cluster > 1 && jobs * cluster > 2 * num_sms()) cluster /= 2;
+  const int64_t piece = (a.max_kv + cluster - 1) / cluster;
+  if (cluster > 1 && piece <= 128) {
+    while (cluster > 1 && (cluster / 2) * 128 >= a.max_kv) cluster /= 2;
+    a.splits = cluster;
+    a.chunk = ((a.max_kv + cluster - 1) / cluster + kKeys - 1) / kKeys * kKeys;
+    a.chunk0 = a.chunk;
+    return a.kv.dh == 128 ? run<128>(a, tiles, cluster > 1, st) : run<64>(a, tiles, cluster > 1, st);
+  }
   // Enough splits for every SM's two CTAs (a wave more when requests may
   // differ in length), of 128 keys at least; long ones in pieces of 2048 keys,
   // so that the last CTAs to finish have little left.
@@ -543,7 +642,7 @@ cudaError_t launch_paged_decode(PagedAttnArgs a, void* ws, cudaStream_t st) {
   a.chunk0 = a.chunk;
   a.splits = static_cast<int>((a.max_kv + a.chunk - 1) / a.chunk);
   paged_partials(&a, ws);
-  const cudaError_t e = a.kv.dh == 128 ? run<128>(a, tiles, st) : run<64>(a, tiles, st);
+  const cudaError_t e = a.kv.dh == 128 ? run<128>(a, tiles, false, st) : run<64>(a, tiles, false, st);
   if (e != cudaSuccess || a.splits == 1) return e;
   return launch_paged_merge(a, st);
 }
