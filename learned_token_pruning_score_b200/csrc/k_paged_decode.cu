@@ -633,7 +633,7 @@ cudaError_t launch_paged_decode(PagedAttnArgs a, void* ws, cudaStream_t st) {
   // Enough splits for every SM's two CTAs (a wave more when requests may
   // differ in length), of 128 keys at least; long ones in pieces of 2048 keys,
   // so that the last CTAs to finish have little left.
-  const int most = paged_max_splits(a.rows, a.batch, a.hq, a.kv.hkv, kRows);
+  const int most = paged_max_splits(a.rows, a.hq, a.kv.dh);
   const int64_t want = std::max<int64_t>(1, (a.batch == 1 ? 2 : 4) * num_sms() / jobs);
   int64_t chunk = std::max<int64_t>(128, (a.max_kv + want - 1) / want);
   if (chunk > 2048) chunk = 2048;

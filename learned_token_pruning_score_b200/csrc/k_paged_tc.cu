@@ -54,15 +54,17 @@ struct Lay {
   // stages of the keys and the rows of A and of B
   static constexpr int kOffAug = 0;
   static constexpr int kOffQ = kSub;                 // A, B
-  static constexpr int kOffK = kOffQ + 2 * kTile;    // 2 stages
-  static constexpr int kOffV = kOffK + 2 * kTile;    // 2 stages
-  static constexpr int kOffBias = kOffV + 2 * kTile; // 4 x 128 fp32
+  // two stages of K and of V at head_dim 128 (32 KB each), four at 64
+  static constexpr int kStages = kDh == 128 ? 2 : 4;
+  static constexpr int kOffK = kOffQ + 2 * kTile;
+  static constexpr int kOffV = kOffK + kStages * kTile;
+  static constexpr int kOffBias = kOffV + kStages * kTile;  // 4 x 128 fp32
   static constexpr int kOffMask = kOffBias + 4 * 512;
   static constexpr int kOffBar = kOffMask + 64;
-  static constexpr size_t kSmem = 1024 + kOffBar + 256;
+  static constexpr size_t kSmem = 1024 + kOffBar + 512;
   static_assert(kSmem <= 232448, "shared memory per CTA");
   // B's output rows wait for the merge in the (by then idle) K tiles
-  static_assert(128 * kDh * 4 == 2 * kTile, "merge buffer");
+  static_assert(128 * kDh * 4 <= kStages * kTile, "merge buffer");
 };
 
 constexpr uint32_t idesc_bmn(int m, int n) { return idesc_bf16_f32(m, n) | (1u << 16); }
@@ -144,17 +146,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* s_bias = reinterpret_cast<float*>(smem + L::kOffBias);        // [4][128]
   uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + L::kOffMask);  // [4][4]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
-  uint64_t* q_full = bars + 0;
-  uint64_t* k_full = bars + 1;    // [2]
-  uint64_t* k_empty = bars + 3;   // [2]
-  uint64_t* v_full = bars + 5;    // [2] the bytes are there
-  uint64_t* v_ready = bars + 7;   // [2] and cleaned
-  uint64_t* v_empty = bars + 9;   // [2]
-  uint64_t* s_full = bars + 11;   // [A, B]
-  uint64_t* p_full = bars + 13;   // [A, B][halves of the keys]
-  uint64_t* o_full = bars + 17;   // [A, B]
-  uint64_t* b_full = bars + 19;   // [4] biases and mask of a tile
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 23);
+  constexpr int kSt = L::kStages;
+  uint64_t* k_full = bars + 0;
+  uint64_t* k_empty = bars + 4;
+  uint64_t* v_full = bars + 8;    // the bytes are there
+  uint64_t* v_ready = bars + 12;  // and cleaned
+  uint64_t* v_empty = bars + 16;
+  uint64_t* b_full = bars + 20;   // [4] biases and mask of a tile
+  uint64_t* p_full = bars + 24;   // [A, B][halves of the keys]
+  uint64_t* s_full = bars + 28;   // [A, B]
+  uint64_t* o_full = bars + 30;   // [A, B]
+  uint64_t* q_full = bars + 32;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 33);
   __shared__ PagedTile s_tile;
   __shared__ int s_found;
   __shared__ float2 s_ml[kBlk];
@@ -168,18 +171,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   if (threadIdx.x == 0) {
     mbar_init(q_full, 256);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 1);
       mbar_init(&v_ready[i], 1);
       mbar_init(&v_empty[i], 1);
+      mbar_init(&b_full[i], 1);
+      mbar_init(&p_full[i], 4);  // the warps of a warpgroup
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&o_full[i], 1);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&p_full[i], 4);  // the warps of a warpgroup
-      mbar_init(&b_full[i], 1);
     }
     fence_mbar_init();
     tma_prefetch_desc(&tmK);
@@ -247,8 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       int pg = page_at(0), pg1 = page_at(1);
       for (int t = 0; t < nt; ++t) {
-        const int s = t & 1;
-        const uint32_t ph = ((t >> 1) & 1) ^ 1;
+        const int s = t % kSt;
+        const uint32_t ph = ((t / kSt) & 1) ^ 1;
         const int pg2 = page_at(t + 2);
         const bool go = mine && pg >= 0;
         const uint32_t bytes =
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto qk = [&](int h, int t) {
         constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
         const uint64_t qd = sdesc_kmajor_sw128(base + L::kOffQ + (h && !both ? L::kTile : 0));
-        const uint64_t kd = sdesc_kmajor_sw128(base + L::kOffK + (t & 1) * L::kTile);
+        const uint64_t kd = sdesc_kmajor_sw128(base + L::kOffK + (t % kSt) * L::kTile);
         const uint32_t d = tm + static_cast<uint32_t>(h * 128);
 #pragma unroll
         for (int kk = 0; kk < kDh / 16; ++kk) {
@@ -292,11 +295,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_f16_ss_warp(d, sdesc_kmajor_sw128(base + L::kOffAug + (h && !both ? 96 : 64)),
                            sdesc_kmajor_sw128(base + L::kOffAug + (t & 1) * 32), idesc, 1u);
         umma_commit_warp(&s_full[h]);
-        if (h == 1 || both) umma_commit_warp(&k_empty[t & 1]);
+        if (h == 1 || both) umma_commit_warp(&k_empty[t % kSt]);
       };
       auto pv = [&](int h, int t, int half, bool first) {
         constexpr uint32_t idesc = idesc_bmn(128, kDh);
-        const uint64_t vd = sdesc_mn(base + L::kOffV + (t & 1) * L::kTile, kSub);
+        const uint64_t vd = sdesc_mn(base + L::kOffV + (t % kSt) * L::kTile, kSub);
         const uint32_t p_tm = tm + static_cast<uint32_t>(h * 128);
         const uint32_t d = tm + 256u + static_cast<uint32_t>(h * 128);
 #pragma unroll
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       auto k_there = [&](int t) -> bool {
-        return mbar_wait_warp(&k_full[t & 1], (t >> 1) & 1, a.err) &&
+        return mbar_wait_warp(&k_full[t % kSt], (t / kSt) & 1, a.err) &&
                (!kBias || mbar_wait_warp(&b_full[t & 3], (t >> 2) & 1, a.err));
       };
       bool ok = mbar_wait_warp(q_full, 0, a.err) && k_there(0);
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int h = decltype(hc)::value;
         const int n = h == 0 ? last_a : last_b;
         const int t = both ? 2 * j + h : j;
-        if ((h == 0 || both) && !mbar_wait_warp(&v_ready[t & 1], (t >> 1) & 1, a.err)) return false;
+        if ((h == 0 || both) && !mbar_wait_warp(&v_ready[t % kSt], (t / kSt) & 1, a.err)) return false;
         // the next keys are there by now: P V and the next S go out back to back
         const bool more = j + 1 < n;
         const int tk = both ? t + 2 : j + 1;
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (more) qk(h, tk);
         else umma_commit_warp(&o_full[h]);
-        if (h == 1 || both) umma_commit_warp(&v_empty[t & 1]);
+        if (h == 1 || both) umma_commit_warp(&v_empty[t % kSt]);
         return true;
       };
       for (int j = 0; j < last_a && ok; ++j) {
@@ -373,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bias_at(t + 1, pg, nb);
         pg = page_at(t + 2);
         // QK(t - 2) has read its K-step; so the softmax of tile t - 4 is over
-        if (!mbar_wait_warp(&k_empty[t & 1], ((t >> 1) & 1) ^ 1, a.err)) break;
+        if (t >= 2 && !mbar_wait_warp(&k_empty[(t - 2) % kSt], ((t - 2) / kSt) & 1, a.err)) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const bool rem = b[i] < kRemovableBias;
@@ -400,8 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!mbar_wait_warp(&b_full[t & 3], (t >> 2) & 1, a.err)) break;
           part = *reinterpret_cast<const uint4*>(s_mask + (t & 3) * 4);
         }
-        const int s = t & 1;
-        if (!mbar_wait_warp(&v_full[s], (t >> 1) & 1, a.err)) break;
+        const int s = t % kSt;
+        if (!mbar_wait_warp(&v_full[s], (t / kSt) & 1, a.err)) break;
         if ((part.x | part.y | part.z | part.w) != 0u || key0 + kBlk > min_limit) {
           uint8_t* v = smem + L::kOffV + s * L::kTile;
           constexpr int kUnits = kDh / 8;  // 16-byte units of a row
@@ -602,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ok = ok && (n_h[h] == 0 || mbar_wait_warp(&o_full[h], 0, a.err));
     if (dual && h == 1) ok = ok && mbar_wait_warp(&o_full[0], 0, a.err);  // all MMAs have read K
     // the last tile's values are cleaned: s_found is final
-    ok = ok && mbar_wait_warp(&v_ready[(nt - 1) & 1], ((nt - 1) >> 1) & 1, a.err);
+    ok = ok && mbar_wait_warp(&v_ready[(nt - 1) % kSt], ((nt - 1) / kSt) & 1, a.err);
     tc_fence_after();
     float4* xo = reinterpret_cast<float4*>(smem + L::kOffK) + r;  // [kDh / 4][128 rows]
     float wa = 1.0f, wb = 0.f;
@@ -706,20 +709,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Splits of the keys, from the sizes that the host knows (requests may be
 // shorter). Times in microseconds, as measured per CTA: a 128-key tile of two
-// warpgroups, the fixed cost of a CTA, the merge with its partial rows.
+// warpgroups (of one, where it waits for memory), the fixed cost of a CTA, the
+// merge with its partial rows.
 void plan(PagedAttnArgs* a) {
   const int64_t sms = num_sms();
   const int group = a->hq / a->kv.hkv;
   const int64_t jobs = a->tiles * a->kv.hkv;
   const int64_t nt = (a->max_kv + kBlk - 1) / kBlk;
   const int64_t mean_rows = a->rows * group / (a->tiles > 0 ? a->tiles : 1);
-  const double tile_us = (mean_rows <= kBlk ? 1.1 : 2.2) * (a->kv.dh == 128 ? 1.0 : 0.8), cta_us = 7.0;
+  const double tile_us = (mean_rows <= kBlk ? 1.6 : 2.2) * (a->kv.dh == 128 ? 1.0 : 0.7), cta_us = 6.0;
   const double part_us = double(a->rows) * a->hq * a->kv.dh * 8.0 / 5.0e6;  // one split's, out and in
-  const int most = paged_max_splits(a->rows, a->batch, a->hq, a->kv.hkv, 2 * kBlk);
+  const int most = paged_max_splits(a->rows, a->hq, a->kv.dh);
   double best = 1e300;
   for (int s = 1; s <= most && s <= nt; ++s) {
     const int64_t c = (nt + s - 1) / s;
-    const double us = double((jobs * s + sms - 1) / sms) * (c * tile_us + cta_us) +
+    const double piece = c * tile_us + cta_us;
+    // one request: whole waves of equal pieces; several, of lengths between
+    // nothing and the longest: their sum, spread over the SMs, and a last piece
+    const double us = (a->batch == 1 ? double((jobs * s + sms - 1) / sms) * piece
+                                     : jobs * (0.6 * nt * tile_us + s * cta_us) / sms + piece) +
                       (s > 1 ? 4.0 + s * part_us : 0.0);
     if (us < best - 1e-9) {
       best = us;
@@ -727,8 +735,9 @@ void plan(PagedAttnArgs* a) {
       a->chunk0 = a->chunk = c * kBlk;
     }
   }
-  // Jobs that leave SMs idle: those take the last tiles of all of them, k each.
-  if (jobs < sms && most >= 2) {
+  // One request that leaves SMs idle: those take the last tiles of all the
+  // others, k each.
+  if (a->batch == 1 && jobs < sms && most >= 2) {
     const int64_t k = (jobs + sms - jobs - 1) / (sms - jobs);
     const double y = (nt * tile_us + cta_us * (1 - k)) / ((k + 1) * tile_us);
     const int64_t tail = static_cast<int64_t>(y);

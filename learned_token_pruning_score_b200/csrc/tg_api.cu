@@ -977,7 +977,7 @@ size_t tg_workspace_size(tg_op op, const tg_shape* s) {
       if (s->dtype != TG_BF16 || s->k < 1 || s->n < 1 || s->n_heads_kv < 1 || s->head_dim < 1 ||
           s->n_heads_q < s->n_heads_kv)
         return 0;
-      return paged_attn_ws_bytes(s->k, s->n, s->n_heads_q, s->n_heads_kv, s->head_dim);
+      return paged_attn_ws_bytes(s->k, s->n_heads_q, s->head_dim);
   }
   return 0;
 }
@@ -1955,9 +1955,9 @@ tg_status paged_view(const tg_paged_kv* c, const int32_t* cu_q, const int32_t* k
 }  // namespace
 
 namespace tg {
-size_t paged_attn_ws_bytes(int64_t rows, int64_t batch, int hq, int hkv, int dh) {
+size_t paged_attn_ws_bytes(int64_t rows, int hq, int dh) {
   // one split writes the output itself
-  const size_t s = paged_max_splits(rows, batch, hq, hkv, paged_tile_rows(rows, batch, hq, hkv));
+  const size_t s = paged_max_splits(rows, hq, dh);
   return s > 1 ? align_up(s * size_t(rows) * size_t(hq) * size_t(dh + 2) * 4, 256) : 256;
 }
 }  // namespace tg
@@ -2060,7 +2060,7 @@ tg_status tg_paged_attn(const tg_paged_kv* cache, const void* q, int64_t q_strid
   a.lse = lse;
   a.err = device_error_word();
   if (dt == TG_BF16) {
-    TG_CHECK(ws != nullptr && ws_bytes >= paged_attn_ws_bytes(rows, batch, hq, hkv, dh),
+    TG_CHECK(ws != nullptr && ws_bytes >= paged_attn_ws_bytes(rows, hq, dh),
              TG_ERR_WORKSPACE);
     TG_CHECK(aligned16(ws), TG_ERR_INVALID_ARG);
   }

@@ -404,15 +404,12 @@ inline int64_t paged_row_tiles(int64_t rows, int64_t batch, int hq, int hkv, int
 inline int paged_tile_rows(int64_t rows, int64_t batch, int hq, int hkv) {
   return rows * (hq / hkv) <= 16 * batch ? 16 : 256;
 }
-// Most splits of a call: up to 64, while the (row tile, KV head, split) jobs
-// stay within 64 (16 rows) or 4 (256 rows) for each of 148 SMs, which also
-// bounds the partial results whatever the batch.
-inline int paged_max_splits(int64_t rows, int64_t batch, int hq, int hkv, int tile) {
-  const int64_t jobs = paged_row_tiles(rows, batch, hq, hkv, tile) * hkv;
-  const int64_t s = (tile == 16 ? 64 : 4) * 148 / (jobs > 0 ? jobs : 1);
+// Most splits of a call: up to 64, while their partial rows stay within 64 MB.
+inline int paged_max_splits(int64_t rows, int hq, int dh) {
+  const int64_t s = (int64_t(64) << 20) / (rows * hq * (dh + 2) * 4 + 1);
   return static_cast<int>(s < 1 ? 1 : s > 64 ? 64 : s);
 }
-size_t paged_attn_ws_bytes(int64_t rows, int64_t batch, int hq, int hkv, int dh);
+size_t paged_attn_ws_bytes(int64_t rows, int hq, int dh);
 // Lays the partial results of a->splits splits out in the workspace.
 inline void paged_partials(PagedAttnArgs* a, void* ws) {
   const size_t n = static_cast<size_t>(a->splits) * a->rows * a->hq;
