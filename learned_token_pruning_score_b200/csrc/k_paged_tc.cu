@@ -11,10 +11,10 @@
 //                   ones, and the two states merge at the end, so that short
 //                   chunks (drafted tokens) keep the tensor core and the loads as
 //                   busy
-// Warps: 0 fetches K and V (lanes walk the page table two tiles ahead), 1 issues
-// the MMAs, 2 allocates TMEM and prepares the keys' gate biases, 3 cleans value
-// rows that must not reach a row, 4-7 softmax A, 8-11 softmax B (one thread a
-// row).
+// Warps: 0 fetches the keys and 3 the values (lanes walk the page table two tiles
+// ahead), 1 issues the MMAs, 2 allocates TMEM, prepares the keys' gate biases and
+// cleans value rows that must not reach a row, 4-7 softmax A, 8-11 softmax B (one
+// thread a row).
 //
 // Per tile and warpgroup: S = Q K^T into 128 TMEM columns, P (bf16) written over
 // S, O += P V with P read from TMEM and V as it lies in the page (keys as K, dh
@@ -235,37 +235,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_h[2] = {dual ? (nt + 1) / 2 : nt, dual ? nt / 2 : nt};
 
   if (warp < 4) {
+    // A tile's boxes (page pieces x 64 columns), one a lane.
+    const int box = min(a.kv.page_size, kBlk);  // rows of a box
+    const int n_box = kBlk / box;               // a power of two
+    const int my_box = lane & (n_box - 1), my_sub = lane / n_box;
+    auto page_at = [&](int t) -> int {  // -1: nothing to fetch; n_pages: reads zeros
+      const int j = lo + t * kBlk + my_box * box;
+      if (t >= nt || j >= hi || my_sub >= L::kSubs) return -1;
+      const int64_t p = page_of(a, tile.req, j);
+      return p < 0 ? static_cast<int>(a.kv.n_pages) : static_cast<int>(p);
+    };
+    auto fetch = [&](const CUtensorMap* tm, uint64_t* full, uint8_t* dst, int t, int pg) {
+      const unsigned live = __popc(__ballot_sync(0xFFFFFFFFu, pg >= 0));
+      if (lane == 0) mbar_arrive_expect_tx(full, live * static_cast<unsigned>(box * 128));
+      __syncwarp();
+      if (pg >= 0)
+        tma_load_4d(tm, full, dst + my_sub * kSub + my_box * box * 128, my_sub * 64, g,
+                    row_in_page(a, lo + t * kBlk + my_box * box), pg);
+    };
     if (warp == 0) {
-      // ------------------------------------------------------------ TMA
-      const int page = a.kv.page_size;
-      const int box = min(page, kBlk);       // rows of a box
-      const int n_box = kBlk / box;          // a power of two
-      const int my_box = lane & (n_box - 1), my_sub = lane / n_box;
-      const bool mine = my_sub < L::kSubs;
-      auto page_at = [&](int t) -> int {  // -1: behind the keys; n_pages: reads zeros
-        const int j = lo + t * kBlk + my_box * box;
-        if (t >= nt || j >= hi) return -1;
-        const int64_t p = page_of(a, tile.req, j);
-        return p < 0 ? static_cast<int>(a.kv.n_pages) : static_cast<int>(p);
-      };
+      // ------------------------------------------------------------ keys
       int pg = page_at(0), pg1 = page_at(1);
       for (int t = 0; t < nt; ++t) {
         const int s = t % kSt;
-        const uint32_t ph = ((t / kSt) & 1) ^ 1;
         const int pg2 = page_at(t + 2);
-        const bool go = mine && pg >= 0;
-        const uint32_t bytes =
-            static_cast<uint32_t>(__popc(__ballot_sync(0xFFFFFFFFu, go)) * box * 128);
-        const int y = row_in_page(a, lo + t * kBlk + my_box * box);
-        const int off = my_sub * kSub + my_box * box * 128;
-        if (!mbar_wait_warp(&k_empty[s], ph, a.err)) break;
-        if (lane == 0) mbar_arrive_expect_tx(&k_full[s], bytes);
-        __syncwarp();
-        if (go) tma_load_4d(&tmK, &k_full[s], smem + L::kOffK + s * L::kTile + off, my_sub * 64, g, y, pg);
-        if (!mbar_wait_warp(&v_empty[s], ph, a.err)) break;
-        if (lane == 0) mbar_arrive_expect_tx(&v_full[s], bytes);
-        __syncwarp();
-        if (go) tma_load_4d(&tmV, &v_full[s], smem + L::kOffV + s * L::kTile + off, my_sub * 64, g, y, pg);
+        if (!mbar_wait_warp(&k_empty[s], ((t / kSt) & 1) ^ 1, a.err)) break;
+        fetch(&tmK, &k_full[s], smem + L::kOffK + s * L::kTile, t, pg);
         pg = pg1;
         pg1 = pg2;
       }
@@ -348,16 +343,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = step(std::integral_constant<int, 0>(), j);
         if (ok && j < last_b) ok = step(std::integral_constant<int, 1>(), j);
       }
-    } else if (warp == 2 && kBias) {
-      // ------------------------------------------------------------ gate biases
+    } else if (warp == 3) {
+      // ------------------------------------------------------------ values
+      int pg = page_at(0), pg1 = page_at(1);
+#pragma unroll 1
+      for (int t = 0; t < nt; ++t) {
+        const int s = t % kSt;
+        const int pg2 = page_at(t + 2);
+        if (!mbar_wait_warp(&v_empty[s], ((t / kSt) & 1) ^ 1, a.err)) break;
+        fetch(&tmV, &v_full[s], smem + L::kOffV + s * L::kTile, t, pg);
+        pg = pg1;
+        pg1 = pg2;
+      }
+    } else {
+      // ------------------------------------------------------------ gate biases, cleaning
       // Keys lane, lane + 32, ... of a tile (rows of their K-step that store
       // without bank conflicts). Lane l holds the page of keys 16 (l & 7) on; pages
       // two tiles ahead, biases one.
-      auto page_at = [&](int t) -> int {
+      auto bias_pages = [&](int t) -> int {
         const int j = lo + t * kBlk + (lane & 7) * 16;
-        return t < nt && j < hi ? static_cast<int>(page_of(a, tile.req, j)) : -1;
+        return kBias && t < nt && j < hi ? static_cast<int>(page_of(a, tile.req, j)) : -1;
       };
-      auto bias_at = [&](int t, int pages, float (&b)[4]) {
+      float b[4];
+      auto load_bias = [&](int t, int pages) {
         const int j = lo + t * kBlk + lane;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -367,43 +375,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : 0.f;
         }
       };
-      float b[4];
-      bias_at(0, page_at(0), b);
-      int pg = page_at(1);
-#pragma unroll 1
-      for (int t = 0; t < nt; ++t) {
-        float nb[4];
-        bias_at(t + 1, pg, nb);
-        pg = page_at(t + 2);
-        // QK(t - 2) has read its K-step; so the softmax of tile t - 4 is over
-        if (t >= 2 && !mbar_wait_warp(&k_empty[(t - 2) % kSt], ((t - 2) / kSt) & 1, a.err)) break;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool rem = b[i] < kRemovableBias;
-          const unsigned bits = __ballot_sync(0xFFFFFFFFu, rem);
-          if (lane == 0) s_mask[(t & 3) * 4 + i] = bits;
-          s_bias[(t & 3) * 128 + lane + 32 * i] = key_bias(b[i]);
-          float b0, b1, b2;
-          split3(rem ? 0.f : b[i], b0, b1, b2);
-          // against (g0, g0, g1, g0, g2, g1)
-          store_aug(smem + L::kOffAug, lane + 32 * i, t & 1, pack_bf16x2(b0, b1), pack_bf16x2(b0, b2),
-                    pack_bf16x2(b0, b1));
-          b[i] = nb[i];
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b_full[t & 3]);
+      int pg = -1;
+      if (kBias) {
+        load_bias(0, bias_pages(0));
+        pg = bias_pages(1);
       }
-    } else if (warp == 3) {
-      // ------------------------------------------------------------ values
-      for (int t = 0; t < nt; ++t) {
-        const int key0 = lo + t * kBlk;
-        uint4 part = make_uint4(0u, 0u, 0u, 0u);  // keys that their bias may remove
-        if (kBias) {
-          if (!mbar_wait_warp(&b_full[t & 3], (t >> 2) & 1, a.err)) break;
-          part = *reinterpret_cast<const uint4*>(s_mask + (t & 3) * 4);
+      // Step i: the biases of tile i, then the values of tile i - 1: the order in
+      // which the MMAs come to need them.
+#pragma unroll 1
+      for (int i = 0; i <= nt; ++i) {
+        if (kBias && i < nt) {
+          // QK(i - 2) has read its K-step; so the softmax of tile i - 4 is over
+          if (i >= 2 && !mbar_wait_warp(&k_empty[(i - 2) % kSt], ((i - 2) / kSt) & 1, a.err)) break;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool rem = b[e] < kRemovableBias;
+            const unsigned bits = __ballot_sync(0xFFFFFFFFu, rem);
+            if (lane == 0) s_mask[(i & 3) * 4 + e] = bits;
+            s_bias[(i & 3) * 128 + lane + 32 * e] = key_bias(b[e]);
+            float b0, b1, b2;
+            split3(rem ? 0.f : b[e], b0, b1, b2);
+            // against (g0, g0, g1, g0, g2, g1)
+            store_aug(smem + L::kOffAug, lane + 32 * e, i & 1, pack_bf16x2(b0, b1), pack_bf16x2(b0, b2),
+                      pack_bf16x2(b0, b1));
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b_full[i & 3]);
+          load_bias(i + 1, pg);
+          pg = bias_pages(i + 2);
         }
-        const int s = t % kSt;
+        const int t = i - 1;
+        if (t < 0) continue;
+        const int s = t % kSt, key0 = lo + t * kBlk;
+        uint4 part = make_uint4(0u, 0u, 0u, 0u);  // keys that their bias may remove
+        if (kBias) part = *reinterpret_cast<const uint4*>(s_mask + (t & 3) * 4);
         if (!mbar_wait_warp(&v_full[s], (t / kSt) & 1, a.err)) break;
         if ((part.x | part.y | part.z | part.w) != 0u || key0 + kBlk > min_limit) {
           uint8_t* v = smem + L::kOffV + s * L::kTile;
@@ -425,8 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (found) s_found = 1;
           fence_async_smem();
+          __syncwarp();
         }
-        __syncwarp();
         if (lane == 0) mbar_arrive(&v_ready[s]);
       }
     }
@@ -435,29 +441,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h = (warp - 4) >> 2;            // warpgroup A or B
     const int r = (threadIdx.x - 128) & 127;  // row of the warpgroup = TMEM lane
     const int rt = (dual ? 0 : h * kBlk) + r; // row of the tile
+    const int w_row = rt - lane;              // the warp's first row
     const bool row_ok = rt < n_rows;
+    // the row's place: token x heads + head (rows x heads of the call: 32 bits)
     const int head = g * group + (row0 + rt) % group;
+    const int tok = tile.tok0 + (row0 + rt) / group;
+    const int at = tok * a.hq + head;
+    const float tau = a.tau && row_ok ? __ldg(a.tau + head) : 1.0f;
+    const float gain = kBias && row_ok ? __ldg(a.gain + head) : 0.0f;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + lane_off + static_cast<uint32_t>(h * 128);
     const uint32_t o_tm = tmem + lane_off + 256u + static_cast<uint32_t>(h * 128);
-    const float tau = a.tau && row_ok ? __ldg(a.tau + head) : 1.0f;
-    const float gain = kBias && row_ok ? __ldg(a.gain + head) : 0.0f;
     const float scale2 = kLog2e / (sqrtf(static_cast<float>(kDh)) * tau);
     // rows without a query see everything (their output goes nowhere)
     const int limit = row_ok ? past + (row0 + rt) / group + 1 : 0x7FFFFFFF;
-    if (!dual || h == 0) {  // this warpgroup's rows of Q, 16 bytes a thread and step
+    if (!dual || h == 0) {  // this warp's rows of Q: 16 bytes a lane, whole rows side by side
       uint8_t* qd = smem + L::kOffQ + (dual ? 0 : h * L::kTile);
-      constexpr int kUnits = kDh / 8;
-#pragma unroll 4
-      for (int e = r; e < kBlk * kUnits; e += kBlk) {
-        const int qr = e / kUnits, u = e % kUnits;
-        const int rr = (dual ? 0 : h * kBlk) + qr;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (rr < n_rows)
-          x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                              static_cast<int64_t>(tile.tok0 + (row0 + rr) / group) * a.q_stride +
-                                              (g * group + (row0 + rr) % group) * kDh + u * 8);
-        *reinterpret_cast<uint4*>(qd + (u >> 3) * kSub + qr * 128 + (((u & 7) ^ (qr & 7)) << 4)) = x;
+      constexpr int kUnits = kDh / 8, kStep = 32 / kUnits;  // 16-byte units of a row
+      const int u = lane % kUnits;
+      const int64_t mine = static_cast<int64_t>(tok) * a.q_stride + head * kDh;
+      uint4 x[kUnits];
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int src = i * kStep + lane / kUnits;
+        const int64_t off = __shfl_sync(0xFFFFFFFFu, mine, src);
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (w_row + src < n_rows)
+          x[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + off + u * 8);
+      }
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int qr = (r - lane) + i * kStep + lane / kUnits;
+        *reinterpret_cast<uint4*>(qd + (u >> 3) * kSub + qr * 128 + (((u & 7) ^ (qr & 7)) << 4)) = x[i];
       }
       if (kBias) {
         float g0, g1, g2;
@@ -633,16 +648,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         l = l * wa + b.y * wb;
       }
     }
-    if (active && ok) {
+    if (active && ok && w_row < n_rows) {
       const bool part = a.splits > 1;
       const bool any = l != 0.f;  // a row that sees nothing is zero
       const float inv = part ? 1.0f : any ? 1.0f / l : 0.f;
+      const int64_t part0 = split * a.rows * a.hq;
       if (row_ok) {
-        const int64_t at = out_row(rt);
         if (part)
-          *reinterpret_cast<float2*>(a.part_ml + (split * a.rows * a.hq + at) * 2) = make_float2(m, l);
+          *reinterpret_cast<float2*>(a.part_ml + (part0 + at) * 2) = make_float2(m, l);
         else if (a.lse != nullptr)
-          a.lse[head * a.rows + tile.tok0 + (row0 + rt) / group] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+          a.lse[head * a.rows + tok] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
       }
       // each warp's 32 rows x 32 columns through its part of the idle Q tile
       uint8_t* stage = smem + L::kOffQ + h * L::kTile + (warp & 3) * 4096;
@@ -687,13 +702,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 8; ++i) {
           const int rr = i * 4 + (lane >> 3), u = lane & 7;
           const float4 f = *reinterpret_cast<const float4*>(stage + rr * 128 + ((u ^ (rr & 7)) << 4));
-          const int ro = (dual ? 0 : h * kBlk) + (warp & 3) * 32 + rr;
-          if (ro < n_rows) {
-            const int64_t at = out_row(ro);
+          const int64_t to = __shfl_sync(0xFFFFFFFFu, at, rr);
+          if (w_row + rr < n_rows) {
             if (part)
-              *reinterpret_cast<float4*>(a.part_o + (split * a.rows * a.hq + at) * kDh + c * 32 + u * 4) = f;
+              *reinterpret_cast<float4*>(a.part_o + (part0 + to) * kDh + c * 32 + u * 4) = f;
             else
-              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at * kDh + c * 32 + u * 4) =
+              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to * kDh + c * 32 + u * 4) =
                   make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
           }
         }
