@@ -639,7 +639,7 @@ tg_status tg_quantize_rows(const void* x, int64_t x_stride, int64_t rows, int32_
  *   y_ij = (sum_k xq_ik wq_jk) xs_i ws_j (+ residual_ij)
  * the sum exact in 32-bit integers, the rest in fp32, rounded once to dtype.
  *   xq [m, k], wq [n, k] int8 (16-byte aligned; any values, -128 included);
- *   xs [m], ws [n] fp32; residual [m, n] dtype or NULL (may equal y);
+ *   xs [m], ws [n] (16-byte aligned) fp32; residual [m, n] dtype or NULL (may equal y);
  *   y [m, n] dtype, bf16 or fp32.
  * n % 32 == 0, k % 16 == 0, k <= 131056 (else TG_ERR_UNSUPPORTED).
  */

@@ -20,28 +20,24 @@
 namespace tg {
 namespace {
 
-__device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
-  const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&u);
+// a 16-byte vector as pairs of fp32
+__device__ __forceinline__ void unpack2(const uint4& u, float2 (&f)[4]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = __bfloat1622float2(e[i]);
-    f[2 * i] = t.x;
-    f[2 * i + 1] = t.y;
-  }
+  for (int i = 0; i < 4; ++i)
+    f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-__device__ __forceinline__ void unpack(const uint4& u, float (&f)[4]) {
-  f[0] = __uint_as_float(u.x);
-  f[1] = __uint_as_float(u.y);
-  f[2] = __uint_as_float(u.z);
-  f[3] = __uint_as_float(u.w);
+__device__ __forceinline__ void unpack2(const uint4& u, float2 (&f)[2]) {
+  f[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+  f[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
 }
-__device__ __forceinline__ uint4 repack(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint4 repack2(const float2 (&f)[4]) {
+  return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
+                    pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
 }
-__device__ __forceinline__ uint4 repack(const float (&f)[4]) {
-  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                    __float_as_uint(f[3]));
+__device__ __forceinline__ uint4 repack2(const float2 (&f)[2]) {
+  return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
+                    __float_as_uint(f[1].y));
 }
 
 // ---------------------------------------------------------------- append
@@ -53,39 +49,68 @@ __device__ __forceinline__ uint4 repack(const float (&f)[4]) {
 // second, so that rotation pairs meet in one thread and the norm needs three
 // shuffles. A CTA takes `tok` tokens: their angles (fp64, from the host's
 // theta_i, so that no thread evaluates a power) go to shared memory first.
-constexpr int kAppThreads = 256;
+// The loads of a CTA's tokens are on their way while pages and angles are found.
+constexpr int kAppThreads = 256, kAppTok = 4;
 
 template <typename T, int kDh>
-__global__ void __launch_bounds__(kAppThreads) paged_append(const __grid_constant__ PagedAppendArgs a,
-                                                            int tok) {
+__global__ void __launch_bounds__(kAppThreads, 3) paged_append(const __grid_constant__ PagedAppendArgs a,
+                                                               int tok) {
   pdl_trigger();
   pdl_wait();
   constexpr int kHalf = kDh / 2;
   constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+  constexpr int kPairs = kVec / 2;
   constexpr int kLanes = kHalf / kVec;           // lanes of one head
   constexpr int kHeads = kAppThreads / kLanes;   // heads of one pass
-  constexpr int kMaxTok = kAppThreads / kHalf;
-  __shared__ __align__(16) float s_cos[kMaxTok][kHalf];
-  __shared__ __align__(16) float s_sin[kMaxTok][kHalf];
-  __shared__ int64_t s_dst_page[kMaxTok];  // page of the token's row, or -1 (skip)
-  __shared__ int s_dst_row[kMaxTok];
-  __shared__ int s_req[kMaxTok];
+  __shared__ __align__(16) float s_cos[kAppTok][kHalf];
+  __shared__ __align__(16) float s_sin[kAppTok][kHalf];
+  __shared__ __align__(16) float s_norm[2][kDh];  // weights of q and k (read as they are aligned)
+  __shared__ int64_t s_dst_page[kAppTok];  // page of the token's row, or -1 (skip)
+  __shared__ int s_dst_row[kAppTok];
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tok;
   const int nt = static_cast<int>(min(static_cast<int64_t>(tok), a.rows - t0));
-  if (threadIdx.x < kMaxTok) s_req[threadIdx.x] = 0;
-  __syncthreads();
+  const int lane = threadIdx.x & 31;
   // request of each token: the number of requests that end at or before it
-  // (cu_q ascends), counted by all threads at once
-  for (int b = threadIdx.x; b < a.batch; b += kAppThreads) {
-    const int64_t end = __ldg(a.cu_q + b + 1);
-    for (int i = 0; i < nt; ++i)
-      if (end <= t0 + i) atomicAdd(&s_req[i], 1);
+  // (cu_q ascends), counted by every warp
+  int req[kAppTok] = {};
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const int64_t end = b0 + lane < a.batch ? __ldg(a.cu_q + b0 + lane + 1) : int64_t(1) << 62;
+#pragma unroll
+    for (int i = 0; i < kAppTok; ++i) req[i] += __popc(__ballot_sync(0xFFFFFFFFu, end <= t0 + i));
   }
-  __syncthreads();
+  const int sub = threadIdx.x % kLanes;
+  const int heads = a.hq + 2 * a.kv.hkv;
+  const int d0 = sub * kVec;
+  // head h0 of token t: q, k and v in turn; rows of no request are not read
+  uint4 ulo[kAppTok], uhi[kAppTok];
+  auto load = [&](int h0) {
+    const T* src = nullptr;
+    int64_t stride = 0;
+    if (h0 < a.hq) {
+      src = static_cast<const T*>(a.q) + h0 * kDh;
+      stride = a.q_stride;
+    } else if (h0 < a.hq + a.kv.hkv) {
+      src = static_cast<const T*>(a.k) + (h0 - a.hq) * kDh;
+      stride = a.k_stride;
+    } else if (h0 < heads) {
+      src = static_cast<const T*>(a.v) + (h0 - a.hq - a.kv.hkv) * kDh;
+      stride = a.v_stride;
+    }
+    src += t0 * stride + d0;
+#pragma unroll
+    for (int i = 0; i < kAppTok; ++i) {
+      ulo[i] = uhi[i] = make_uint4(0, 0, 0, 0);
+      if (i < nt && h0 < heads && req[i] < a.batch) {
+        ulo[i] = *reinterpret_cast<const uint4*>(src + i * stride);
+        uhi[i] = *reinterpret_cast<const uint4*>(src + i * stride + kHalf);
+      }
+    }
+  };
+  load(threadIdx.x / kLanes);
   if (threadIdx.x < nt) {
     const int i = threadIdx.x;
     const int64_t t = t0 + i;
-    const int b = s_req[i];
+    const int b = i == 0 ? req[0] : i == 1 ? req[1] : i == 2 ? req[2] : req[3];
     int64_t page = -1;
     int row = 0;
     bool bad = false;
@@ -109,6 +134,10 @@ __global__ void __launch_bounds__(kAppThreads) paged_append(const __grid_constan
     if (page >= 0 && a.kv.bias != nullptr)
       a.kv.bias[page * a.kv.bias_page_stride + row] = a.s ? logsigmoid_f(__ldg(a.s + t)) : 0.0f;
   }
+  if (threadIdx.x < kDh) {
+    if (a.q_norm != nullptr) s_norm[0][threadIdx.x] = __ldg(a.q_norm + threadIdx.x);
+    if (a.k_norm != nullptr) s_norm[1][threadIdx.x] = __ldg(a.k_norm + threadIdx.x);
+  }
   if (a.rotate) {
     for (int e = threadIdx.x; e < nt * kHalf; e += kAppThreads) {
       const int i = e / kHalf, f = e % kHalf;
@@ -116,7 +145,7 @@ __global__ void __launch_bounds__(kAppThreads) paged_append(const __grid_constan
       if (a.pos != nullptr) {
         pos = __ldg(a.pos + t0 + i);
       } else {  // the row's index in its request
-        const int b = s_req[i];
+        const int b = i == 0 ? req[0] : i == 1 ? req[1] : i == 2 ? req[2] : req[3];
         const int64_t t = t0 + i;
         pos = b < a.batch ? static_cast<int64_t>(__ldg(a.kv_len + b)) - __ldg(a.cu_q + b + 1) + t : 0;
       }
@@ -126,73 +155,79 @@ __global__ void __launch_bounds__(kAppThreads) paged_append(const __grid_constan
     }
   }
   __syncthreads();
-  const int sub = threadIdx.x % kLanes;
-  const int heads = a.hq + 2 * a.kv.hkv;
-  const int d0 = sub * kVec;
-  for (int i = 0; i < nt; ++i) {
-    if (s_req[i] >= a.batch) continue;
-    const int64_t t = t0 + i;
-    const int64_t page = s_dst_page[i];
-    const int row = s_dst_row[i];
-    for (int h0 = threadIdx.x / kLanes; h0 < ((heads + kHeads - 1) / kHeads) * kHeads; h0 += kHeads) {
-      const bool on = h0 < heads;  // every lane of the warp reaches the shuffles
-      const int kind = h0 < a.hq ? 0 : (h0 < a.hq + a.kv.hkv ? 1 : 2);
-      const int h = kind == 0 ? h0 : (kind == 1 ? h0 - a.hq : h0 - a.hq - a.kv.hkv);
-      const T* src = nullptr;
-      T* dst = nullptr;
-      if (on && kind == 0) {
-        src = static_cast<const T*>(a.q) + t * a.q_stride + h * kDh;
-        dst = static_cast<T*>(a.q_out) + (t * a.hq + h) * kDh;
-      } else if (on && page >= 0) {
-        src = static_cast<const T*>(kind == 1 ? a.k : a.v) + t * (kind == 1 ? a.k_stride : a.v_stride) +
-              h * kDh;
-        dst = static_cast<T*>(kind == 1 ? a.kv.k : a.kv.v) +
-              page * (kind == 1 ? a.kv.k_page_stride : a.kv.v_page_stride) +
-              (static_cast<int64_t>(row) * a.kv.hkv + h) * kDh;
-      }
-      uint4 ulo = make_uint4(0, 0, 0, 0), uhi = ulo;
-      if (src != nullptr) {
-        ulo = *reinterpret_cast<const uint4*>(src + d0);
-        uhi = *reinterpret_cast<const uint4*>(src + kHalf + d0);
-      }
-      const float* nw = kind == 0 ? a.q_norm : (kind == 1 ? a.k_norm : nullptr);
-      if (a.q_norm != nullptr || a.k_norm != nullptr || a.rotate) {
-        float lo[kVec], hi[kVec];
-        unpack(ulo, lo);
-        unpack(uhi, hi);
-        float ss = 0.f;
+  // every lane of a warp reaches the shuffles
+  for (int pass = 0; pass < heads; pass += kHeads) {
+    const int h0 = pass + threadIdx.x / kLanes;
+    if (pass > 0) load(h0);
+    const int kind = h0 < a.hq ? 0 : (h0 < a.hq + a.kv.hkv ? 1 : 2);
+    const int h = kind == 0 ? h0 : (kind == 1 ? h0 - a.hq : h0 - a.hq - a.kv.hkv);
+    const bool norm = kind == 0 ? a.q_norm != nullptr : (kind == 1 && a.k_norm != nullptr);
+    const float* nw = s_norm[kind == 0 ? 0 : 1];
+    const bool work = a.q_norm != nullptr || a.k_norm != nullptr || a.rotate;
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) ss += lo[e] * lo[e] + hi[e] * hi[e];
+    for (int i = 0; i < kAppTok; ++i) {
+      if (i >= nt) break;
+      const int64_t t = t0 + i;
+      if (work) {
+        float2 lo[kPairs], hi[kPairs];
+        unpack2(ulo[i], lo);
+        unpack2(uhi[i], hi);
+        if (a.q_norm != nullptr || a.k_norm != nullptr) {
+          float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        if (nw != nullptr) {
-          const float r = rsqrtf(ss * (1.0f / kDh) + a.eps);
+          for (int e = 0; e < kPairs; ++e) s2 = ffma2(lo[e], lo[e], ffma2(hi[e], hi[e], s2));
+          float ss = s2.x + s2.y;
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) {
-            lo[e] = lo[e] * r * __ldg(nw + d0 + e);
-            hi[e] = hi[e] * r * __ldg(nw + kHalf + d0 + e);
+          for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+          if (norm) {
+            const float r = rsqrtf(ss * (1.0f / kDh) + a.eps);
+            const float2 r2 = make_float2(r, r);
+            const float2* wl = reinterpret_cast<const float2*>(nw + d0);
+            const float2* wh = reinterpret_cast<const float2*>(nw + kHalf + d0);
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) {
+              lo[e] = fmul2(fmul2(lo[e], r2), wl[e]);
+              hi[e] = fmul2(fmul2(hi[e], r2), wh[e]);
+            }
           }
         }
         if (kind < 2) {
           if (a.rotate) {
+            const float2* cs = reinterpret_cast<const float2*>(&s_cos[i][d0]);
+            const float2* sn = reinterpret_cast<const float2*>(&s_sin[i][d0]);
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-              const float c = s_cos[i][d0 + e], s = s_sin[i][d0 + e];
-              const float x = lo[e], y = hi[e];
-              lo[e] = x * c - y * s;
-              hi[e] = y * c + x * s;
+            for (int e = 0; e < kPairs; ++e) {
+              const float2 c = cs[e], s = sn[e], x = lo[e], y = hi[e];
+              lo[e] = ffma2(x, c, fmul2(y, make_float2(-s.x, -s.y)));
+              hi[e] = ffma2(y, c, fmul2(x, s));
             }
           }
-          ulo = repack(lo);
-          uhi = repack(hi);
+          ulo[i] = repack2(lo);
+          uhi[i] = repack2(hi);
         }
       }
-      if (dst != nullptr) {
-        *reinterpret_cast<uint4*>(dst + d0) = ulo;
-        *reinterpret_cast<uint4*>(dst + kHalf + d0) = uhi;
+      if (req[i] >= a.batch || h0 >= heads) continue;
+      T* dst;
+      if (kind == 0) {
+        dst = static_cast<T*>(a.q_out) + (t * a.hq + h) * kDh;
+      } else {
+        const int64_t page = s_dst_page[i];
+        if (page < 0) continue;
+        dst = static_cast<T*>(kind == 1 ? a.kv.k : a.kv.v) +
+              page * (kind == 1 ? a.kv.k_page_stride : a.kv.v_page_stride) +
+              (static_cast<int64_t>(s_dst_row[i]) * a.kv.hkv + h) * kDh;
       }
+      *reinterpret_cast<uint4*>(dst + d0) = ulo[i];
+      *reinterpret_cast<uint4*>(dst + kHalf + d0) = uhi[i];
     }
   }
+}
+
+__device__ __forceinline__ void unpack4(const uint4& u, float (&f)[4]) {
+  f[0] = __uint_as_float(u.x);
+  f[1] = __uint_as_float(u.y);
+  f[2] = __uint_as_float(u.z);
+  f[3] = __uint_as_float(u.w);
 }
 
 // ---------------------------------------------------------------- attention, CUDA cores
@@ -246,7 +281,7 @@ __global__ void __launch_bounds__(kSimtThreads)
                                           static_cast<int64_t>(tile.tok0 + rr / group) * a.q_stride +
                                           (g * group + rr % group) * kDh + c);
     }
-    unpack(u, f);
+    unpack4(u, f);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) sm.q[r][c + i] = f[i];
   }
@@ -289,8 +324,8 @@ __global__ void __launch_bounds__(kSimtThreads)
             b = key_bias(a.kv.bias[page * a.kv.bias_page_stride + row_in_page(a, j)]);
         }
       }
-      unpack(uk, fk);
-      unpack(uv, fv);
+      unpack4(uk, fk);
+      unpack4(uv, fv);
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
         sm.k[r][c + i] = fk[i];
@@ -396,11 +431,9 @@ __global__ void __launch_bounds__(kSimtThreads)
 
 template <typename T, int kDh>
 cudaError_t run_append(const PagedAppendArgs& a, cudaStream_t st) {
-  constexpr int kMaxTok = kAppThreads / (kDh / 2);
-  // one token per CTA until every SM has several CTAs, then as many as one
-  // pass of angles covers
+  // one token per CTA until every SM has several CTAs
   int tok = 1;
-  while (tok < kMaxTok && a.rows / (2 * tok) >= 8 * num_sms()) tok *= 2;
+  while (tok < kAppTok && a.rows / (2 * tok) >= 6 * num_sms()) tok *= 2;
   const unsigned grid = static_cast<unsigned>((a.rows + tok - 1) / tok);
   TG_CUDA_TRY(launch_pdl(paged_append<T, kDh>, dim3(grid), dim3(kAppThreads), 0, st, a, tok));
   return cudaGetLastError();

@@ -1,6 +1,8 @@
 // k_quant.cu -- 8-bit integer rows for the projections: quantisation with one
 // scale per row (tg_quantize_rows) and the CUDA-core product
 // (tg_linear_quantized with few rows).
+#include <algorithm>
+
 #include "tg_device.cuh"
 #include "tg_internal.h"
 
@@ -9,89 +11,158 @@ namespace {
 
 // ---------------------------------------------------------------- quantisation
 // amax = max |x|, scale = amax / 127, xq = rint(127 x / amax) (ties to even).
-// The integer is the one of the exact quotient: y = x * (127 / amax) in fp32
-// is off by at most 127 * 1.5 * 2^-23 < 3e-5, so a y farther than 1e-4 from
-// every half-integer rounds as the exact quotient does, and the few others
-// are divided in fp64, where 127 x is exact and the rounded quotient (of a
-// 31-bit by a 24-bit integer, at most 2^8 large) falls on the right side of
-// the half-integer, or on it.
+// Bound by HBM: each row is read once (held in registers) and written once.
+// That leaves about ten instructions an element: t = fma(x, 127 / amax, 1.5 *
+// 2^23) has the rounded integer in its low bits, and e = x * 127 / amax minus
+// it says how near the border it was. The integer is the one of the exact
+// quotient: 127 / amax is rounded (2^-24 relative), so the product is off by at
+// most 127 * 2^-24 < 8e-6, and where |e| is within 1e-5 of a half (0.4% of bf16
+// values: quotients of 8-bit mantissas often are ties) the side is decided
+// exactly. (Each such quotient in fp64 instead: 171 us for 32768 x 6144.)
 template <typename T>
 struct Vec16;
 template <>
 struct Vec16<__nv_bfloat16> {
   static constexpr int kN = 8;
-  static __device__ __forceinline__ void get(const uint4& u, float (&f)[8]) {
-    const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 t = __bfloat1622float2(e[i]);
-      f[2 * i] = t.x;
-      f[2 * i + 1] = t.y;
-    }
+  // elements 4 i .. 4 i + 3 of a 16-byte vector
+  static __device__ __forceinline__ void get4(const uint4& u, int i, float (&f)[4]) {
+    const uint32_t a = i == 0 ? u.x : u.z, b = i == 0 ? u.y : u.w;
+    f[0] = __uint_as_float(a << 16);
+    f[1] = __uint_as_float(a & 0xFFFF0000u);
+    f[2] = __uint_as_float(b << 16);
+    f[3] = __uint_as_float(b & 0xFFFF0000u);
+  }
+  // running largest magnitudes, of the even and the odd elements (a NaN stays)
+  using Top = __nv_bfloat162;
+  static __device__ __forceinline__ Top none() { return __floats2bfloat162_rn(0.f, 0.f); }
+  static __device__ __forceinline__ Top top(const uint4& u, Top m) {
+    const Top* e = reinterpret_cast<const Top*>(&u);
+    return __hmax2_nan(__hmax2_nan(m, __hmax2_nan(__habs2(e[0]), __habs2(e[1]))),
+                       __hmax2_nan(__habs2(e[2]), __habs2(e[3])));
+  }
+  // as the bits of an fp32 magnitude
+  static __device__ __forceinline__ uint32_t bits(Top m) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(&m) & 0x7FFF7FFFu;
+    return max(w << 16, w & 0xFFFF0000u);
   }
 };
 template <>
 struct Vec16<float> {
   static constexpr int kN = 4;
-  static __device__ __forceinline__ void get(const uint4& u, float (&f)[4]) {
+  static __device__ __forceinline__ void get4(const uint4& u, int, float (&f)[4]) {
     f[0] = __uint_as_float(u.x);
     f[1] = __uint_as_float(u.y);
     f[2] = __uint_as_float(u.z);
     f[3] = __uint_as_float(u.w);
   }
+  using Top = uint32_t;
+  static __device__ __forceinline__ Top none() { return 0u; }
+  static __device__ __forceinline__ Top top(const uint4& u, Top m) {
+    return max(m, max(max(u.x & 0x7FFFFFFFu, u.y & 0x7FFFFFFFu), max(u.z & 0x7FFFFFFFu, u.w & 0x7FFFFFFFu)));
+  }
+  static __device__ __forceinline__ uint32_t bits(Top m) { return m; }
 };
 
-__device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7FFFFFFFu; }
-
-__device__ __forceinline__ int quantize_one(float x, float r, float amax) {
-  const float y = x * r;
-  const float q = rintf(y);
-  if (fabsf(fabsf(y - q) - 0.5f) < 1e-4f || !(fabsf(y) < 128.0f))
-    return static_cast<int>(rint(127.0 * static_cast<double>(x) / static_cast<double>(amax)));
-  return static_cast<int>(q);
+// The integer of 127 x / amax where the product x r may be on the wrong side of a
+// border (amax within 2^+-64 of 1, r = 127 / amax rounded): c is the border, and
+// the sign of 127 x - c amax comes from two exact parts of the product c amax.
+__device__ __forceinline__ uint32_t quantize_exact(float x, float r, float amax) {
+  constexpr float kMagic = 12582912.0f;
+  float q = fmaf(x, r, kMagic) - kMagic;
+  const float e = fmaf(x, r, -q);
+  if (fabsf(e) > 0.49999f) {
+    const float c = q + copysignf(0.5f, e);
+    const float hi = c * amax, lo = fmaf(c, amax, -hi), d = fmaf(127.0f, x, -hi);
+    q = d > lo ? c + 0.5f : d < lo ? c - 0.5f : rintf(c);
+  }
+  return __float_as_uint(q + kMagic);
 }
 
-template <typename T>
+struct QuantRow {
+  float r;             // 127 / amax
+  float shift;         // 1, or the power of two that brings amax near 1
+  float r_near, amax;  // after it
+};
+
+// Four integers in a word.
+__device__ __forceinline__ uint32_t quantize4(const float (&f)[4], const QuantRow& a) {
+  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
+  uint32_t q[4];
+  float e[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float t = fmaf(f[i], a.r, kMagic);
+    q[i] = __float_as_uint(t);
+    e[i] = fabsf(fmaf(f[i], a.r, kMagic - t));
+  }
+  const float worst = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
+  if (!(worst <= 0.49999f)) {  // (127 / amax infinite: NaN, or 1e7 and more)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = quantize_exact(f[i] * a.shift, a.r_near, a.amax);
+  }
+  return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+}
+
+// kWarps warps a row; the first kHold vectors of each thread stay in registers.
+template <typename T, int kWarps, int kHold>
 __global__ void __launch_bounds__(256) quantize_rows(const T* __restrict__ x, int64_t x_stride,
                                                      int64_t rows, int cols, int8_t* __restrict__ xq,
                                                      float* __restrict__ scale) {
   using V = Vec16<T>;
+  constexpr int kThreads = kWarps * 32;
+  __shared__ uint32_t s_max[8];
   pdl_trigger();
   pdl_wait();
-  __shared__ uint32_t s_max[8];
-  const int64_t row = blockIdx.x;
-  const uint4* src = reinterpret_cast<const uint4*>(x + row * x_stride);
-  const int n_vec = cols / V::kN;
-  uint32_t mx = 0;
-  for (int i = threadIdx.x; i < n_vec; i += blockDim.x) {
-    float f[V::kN];
-    V::get(src[i], f);
+  const int tid = threadIdx.x % kThreads;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (8 / kWarps) + threadIdx.x / kThreads;
+  const bool on = row < rows;
+  const uint4* src = reinterpret_cast<const uint4*>(x + (on ? row : 0) * x_stride);
+  const int n_vec = on ? cols / V::kN : 0;
+  uint4 u[kHold];
 #pragma unroll
-    for (int j = 0; j < V::kN; ++j) mx = max(mx, abs_bits(f[j]));
+  for (int i = 0; i < kHold; ++i) {
+    const int at = tid + i * kThreads;
+    u[i] = at < n_vec ? __ldg(src + at) : make_uint4(0u, 0u, 0u, 0u);
   }
-  mx = __reduce_max_sync(0xFFFFFFFFu, mx);
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = mx;
-  __syncthreads();
-  mx = 0;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) mx = max(mx, s_max[w]);
+  typename V::Top top = V::none();
+#pragma unroll
+  for (int i = 0; i < kHold; ++i) top = V::top(u[i], top);
+  for (int at = tid + kHold * kThreads; at < n_vec; at += kThreads) top = V::top(__ldg(src + at), top);
+  uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, V::bits(top));
+  if constexpr (kWarps > 1) {
+    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = mx;
+    __syncthreads();
+    const int w0 = threadIdx.x / kThreads * kWarps;
+    mx = s_max[w0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) mx = max(mx, s_max[w0 + w]);
+  }
+  if (!on) return;
   const bool finite = mx < 0x7F800000u;
   const float amax = __uint_as_float(mx);
-  if (threadIdx.x == 0) scale[row] = finite ? amax / 127.0f : __uint_as_float(0x7FC00000u);
+  if (tid == 0) scale[row] = finite ? amax / 127.0f : __uint_as_float(0x7FC00000u);
   const bool zero = !finite || mx == 0;
-  const float r = 127.0f / amax;
+  QuantRow a;
+  a.r = 127.0f / amax;
+  a.shift = amax < 5.4210109e-20f ? 1.8446744e19f : amax > 1.8446744e19f ? 5.4210109e-20f : 1.0f;  // 2^+-64
+  a.amax = amax * a.shift;
+  a.r_near = 127.0f / a.amax;
   uint32_t* dst = reinterpret_cast<uint32_t*>(xq + row * cols);
-  for (int i = threadIdx.x; i < n_vec; i += blockDim.x) {
-    float f[V::kN];
-    V::get(src[i], f);
+  auto put = [&](const uint4& w, int at) {
+    uint32_t q[V::kN / 4];
 #pragma unroll
-    for (int j = 0; j < V::kN; j += 4) {
-      uint32_t w = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w |= (static_cast<uint32_t>(zero ? 0 : quantize_one(f[j + e], r, amax)) & 255u) << (8 * e);
-      dst[i * (V::kN / 4) + j / 4] = w;
+    for (int i = 0; i < V::kN / 4; ++i) {
+      float f[4];
+      V::get4(w, i, f);
+      q[i] = zero ? 0u : quantize4(f, a);
     }
-  }
+    if constexpr (V::kN == 8) *reinterpret_cast<uint2*>(dst + 2 * at) = make_uint2(q[0], q[1]);
+    else dst[at] = q[0];
+  };
+#pragma unroll
+  for (int i = 0; i < kHold; ++i)
+    if (tid + i * kThreads < n_vec) put(u[i], tid + i * kThreads);
+  for (int at = tid + kHold * kThreads; at < n_vec; at += kThreads) put(__ldg(src + at), at);
 }
 
 // ---------------------------------------------------------------- product, few rows
@@ -156,17 +227,30 @@ __global__ void __launch_bounds__(256) quant_gemv(const __grid_constant__ QuantG
 
 }  // namespace
 
+template <typename T>
+static cudaError_t run_quantize(const T* x, int64_t x_stride, int64_t rows, int cols, int8_t* xq,
+                                float* scale, cudaStream_t st) {
+  // as few warps a row as hold it in three or four vectors a thread (32768 x 6144
+  // on 8 warps: 110 us with three, 119 with four of which one is empty)
+  const int n_vec = cols / Vec16<T>::kN;
+  auto go = [&](auto kern, int warps) {
+    const int per = 8 / warps;
+    return launch_pdl(kern, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(256), 0, st, x,
+                      x_stride, rows, cols, xq, scale);
+  };
+  if (n_vec <= 128) return go(quantize_rows<T, 1, 4>, 1);
+  if (n_vec <= 256) return go(quantize_rows<T, 2, 4>, 2);
+  if (n_vec <= 512) return go(quantize_rows<T, 4, 4>, 4);
+  if (n_vec <= 768) return go(quantize_rows<T, 8, 3>, 8);
+  return go(quantize_rows<T, 8, 4>, 8);
+}
+
 cudaError_t launch_quantize_rows(const void* x, int64_t x_stride, int64_t rows, int cols, bool bf16,
                                  int8_t* xq, float* scale, cudaStream_t st) {
   if (rows <= 0) return cudaSuccess;
-  const dim3 grid(static_cast<unsigned>(rows));
   if (bf16)
-    TG_CUDA_TRY(launch_pdl(quantize_rows<__nv_bfloat16>, grid, dim3(256), 0, st,
-                           static_cast<const __nv_bfloat16*>(x), x_stride, rows, cols, xq, scale));
-  else
-    TG_CUDA_TRY(launch_pdl(quantize_rows<float>, grid, dim3(256), 0, st,
-                           static_cast<const float*>(x), x_stride, rows, cols, xq, scale));
-  return cudaGetLastError();
+    return run_quantize(static_cast<const __nv_bfloat16*>(x), x_stride, rows, cols, xq, scale, st);
+  return run_quantize(static_cast<const float*>(x), x_stride, rows, cols, xq, scale, st);
 }
 
 cudaError_t launch_quant_gemm(const QuantGemmArgs& g, cudaStream_t st) {

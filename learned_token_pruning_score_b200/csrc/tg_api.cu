@@ -2096,7 +2096,7 @@ tg_status tg_linear_quantized(const int8_t* xq, const float* xs, const int8_t* w
   TG_CHECK((m == 0 || (xq && xs && y)) && wq && ws && m >= 0 && m < (int64_t(1) << 31) && n >= 1 && k >= 1,
            TG_ERR_INVALID_ARG);
   TG_CHECK(n % 32 == 0 && k % 16 == 0 && k <= 131056, TG_ERR_UNSUPPORTED);
-  TG_CHECK(aligned16(xq) && aligned16(wq) && aligned16(y) && aligned16(residual),
+  TG_CHECK(aligned16(xq) && aligned16(wq) && aligned16(ws) && aligned16(y) && aligned16(residual),
            TG_ERR_INVALID_ARG);
   const QuantGemmArgs g{xq, xs, wq, ws, residual, y, m, n, k, dt == TG_BF16};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
