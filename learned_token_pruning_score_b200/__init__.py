@@ -12,7 +12,6 @@ it raises ImportError -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from dataclasses import dataclass
 from typing import Dict, List, Optional, Sequence
@@ -27,6 +26,11 @@ if not os.path.exists(LIB_PATH):
         f"{LIB_PATH} is not built; run `python learned_token_pruning_score_b200/_build.py`")
 
 _lib = ctypes.CDLL(LIB_PATH)
+try:
+    from . import _binding  # noqa: E402  (links against the library just loaded)
+except ImportError as e:
+    raise ImportError(f"{_HERE}/_binding.so is not built, or not for this torch; run `python "
+                      f"learned_token_pruning_score_b200/_build.py` ({e})") from e
 
 # ----------------------------------------------------------------- ABI types
 
@@ -668,71 +672,21 @@ def tg_prefill_batch(model: Model, x, protect, lens: Sequence[int], ks: Sequence
 
 # ----------------------------------------------------------------- paged cache
 #
-# These calls are made once a layer and token, where the kernel takes a few
-# microseconds: their checks form no message unless they fail.
-
-_cur_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
-_cur_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# These calls are made once a layer and token, where the kernels take a few
+# microseconds; their checks, allocations and the call of the ABI are in the
+# extension module (csrc/binding.cpp).
 
 
-def _stream_at(stream, index: int):
-    """_stream for the device `index`."""
+def _handle(stream):
+    """A stream as the extension takes it: None or its handle."""
     if stream is None:
-        if _cur_stream is not None:
-            return _cur_stream(index)
-        return torch.cuda.current_stream(index).cuda_stream
+        return None
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _call(index: int, fn, name: str, *args) -> None:
-    """fn(*args) with device `index` as the current one."""
-    cur = _cur_device() if _cur_device is not None else torch.cuda.current_device()
-    if cur == index:
-        status = fn(*args)
-    else:
-        with torch.cuda.device(index):
-            status = fn(*args)
-    if status != TG_OK:
-        raise TokenGateError(status, name)
 
 
 def _need(cond: bool, what: str) -> None:
     if not cond:
         raise ValueError(what)
-
-
-def _device_index(t: torch.Tensor) -> int:
-    index = t.get_device()
-    if index < 0:
-        raise ValueError("tensors must be on a CUDA device")
-    return index
-
-
-def _vec(t, n: int, dtype, index: int, name: str):
-    """Pointer of an optional contiguous 1-D tensor of n elements."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.get_device() != index or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on cuda:{index}")
-    return t.data_ptr()
-
-
-def _rows3(t, rows: int, heads: int, dh: int, dtype, index: int, name: str) -> int:
-    """Row stride of a [rows, heads, dh] tensor whose rows are contiguous."""
-    if t.dtype is not dtype or t.get_device() != index or t.shape != (rows, heads, dh):
-        raise ValueError(f"{name} must be {dtype} [{rows}, {heads}, {dh}] on cuda:{index}")
-    if rows == 0:
-        return heads * dh
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != dh and heads != 1):
-        raise ValueError(f"{name}: each row must be contiguous")
-    return s0 if rows > 1 else max(s0, heads * dh)
-
-
-@functools.lru_cache(maxsize=1024)
-def _paged_ws_bytes(batch: int, rows: int, hq: int, hkv: int, dh: int, dtype: int) -> int:
-    return tg_workspace_size(TG_OP_PAGED_ATTN, n=batch, k=rows, n_heads_q=hq, n_heads_kv=hkv,
-                             head_dim=dh, dtype=dtype)
 
 
 class PagedKV:
@@ -769,8 +723,7 @@ class PagedKV:
                            table.data_ptr(), n_pages, apart(k, page), apart(v, page),
                            0 if bias is None else apart(bias, ps), table.shape[1], ps, hkv, dh,
                            _dt(k))
-        self._ref = ctypes.byref(self.c)
-        self._index, self._tg_dtype = k.get_device(), self.c.dtype
+        self._h = _binding.cache(ctypes.addressof(self.c), k.get_device(), self.batch)
 
 
 def tg_paged_append(cache: PagedKV, k, v, cu_q, kv_len, q=None, pos=None, s=None, q_norm=None,
@@ -783,31 +736,11 @@ def tg_paged_append(cache: PagedKV, k, v, cu_q, kv_len, q=None, pos=None, s=None
     None, all possibly slices of one fused projection; cu_q [batch + 1],
     kv_len [batch] (the new rows included) int32. Returns the rotated queries
     [rows, hq, dh], or None without q."""
-    index, dt, dh, nb = _device_index(cache.k), cache.dtype, cache.head_dim, cache.batch
-    hkv, rows = cache.n_heads_kv, k.shape[0]
-    k_st = _rows3(k, rows, hkv, dh, dt, index, "k")
-    v_st = _rows3(v, rows, hkv, dh, dt, index, "v")
-    hq = q_st = 0
-    q_ptr = out_ptr = None
-    if q is not None:
-        hq = q.shape[1]
-        q_st = _rows3(q, rows, hq, dh, dt, index, "q")
-        if q_out is None:
-            q_out = torch.empty((rows, hq, dh), dtype=dt, device=cache.device)
-        elif (q_out.shape != (rows, hq, dh) or q_out.dtype is not dt or q_out.get_device() != index
-              or not q_out.is_contiguous()):
-            raise ValueError("q_out must be contiguous, as q in shape and dtype")
-        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    i32, f32 = torch.int32, torch.float32
-    _call(index, _paged_append, "tg_paged_append", cache._ref, q_ptr, q_st, k.data_ptr(), k_st,
-          v.data_ptr(), v_st, rows, _vec(cu_q, nb + 1, i32, index, "cu_q"),
-          _vec(kv_len, nb, i32, index, "kv_len"), nb, hq, _vec(pos, rows, i32, index, "pos"),
-          _vec(s, rows, f32, index, "s"), _vec(q_norm, dh, f32, index, "q_norm"),
-          _vec(k_norm, dh, f32, index, "k_norm"), eps, rope_base, out_ptr,
-          _stream_at(stream, index))
-    return q_out
+    r = _binding.paged_append(cache._h, k, v, cu_q, kv_len, q, pos, s, q_norm, k_norm, eps,
+                              rope_base, q_out, _handle(stream))
+    if r.__class__ is int:
+        raise TokenGateError(r, "tg_paged_append")
+    return r
 
 
 def tg_paged_attn(cache: PagedKV, q, cu_q, kv_len, gain=None, tau=None,
@@ -817,26 +750,12 @@ def tg_paged_attn(cache: PagedKV, q, cu_q, kv_len, gain=None, tau=None,
     dh] rotated; gain, tau [hq] fp32; max_kv: an upper bound of kv_len (None:
     the table's capacity). lse [hq, rows] fp32 is written when given. Returns
     out [rows, hq, dh]."""
-    index, dt, dh, nb = _device_index(cache.k), cache.dtype, cache.head_dim, cache.batch
-    rows, hq = q.shape[0], q.shape[1]
-    q_st = _rows3(q, rows, hq, dh, dt, index, "q")
-    if out is None:
-        out = torch.empty((rows, hq, dh), dtype=dt, device=cache.device)
-    elif (out.shape != (rows, hq, dh) or out.dtype is not dt or out.get_device() != index
-          or not out.is_contiguous()):
-        raise ValueError("out must be contiguous, as q in shape and dtype")
-    need = _paged_ws_bytes(nb, rows, hq, cache.n_heads_kv, dh, cache._tg_dtype)
-    ws_ptr, ws_bytes = None, 0
-    if need > 0 or ws is not None:
-        ws = _ws(need, cache.device, ws)
-        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-    i32, f32 = torch.int32, torch.float32
-    _call(index, _paged_attn, "tg_paged_attn", cache._ref, q.data_ptr(), q_st, rows,
-          _vec(cu_q, nb + 1, i32, index, "cu_q"), _vec(kv_len, nb, i32, index, "kv_len"), nb, hq,
-          cache.capacity if max_kv is None else int(max_kv), _vec(gain, hq, f32, index, "gain"),
-          _vec(tau, hq, f32, index, "tau"), out.data_ptr(), _vec(lse, hq * rows, f32, index, "lse"),
-          ws_ptr, ws_bytes, _stream_at(stream, index))
-    return out
+    r = _binding.paged_attn(cache._h, q, cu_q, kv_len, gain, tau,
+                            cache.capacity if max_kv is None else int(max_kv), out, lse, ws,
+                            _handle(stream))
+    if r.__class__ is int:
+        raise TokenGateError(r, "tg_paged_attn")
+    return r
 
 
 # ----------------------------------------------------------------- 8-bit projections
@@ -845,50 +764,23 @@ def tg_paged_attn(cache: PagedKV, q, cu_q, kv_len, gain=None, tau=None,
 def tg_quantize_rows(x, xq=None, scale=None, stream=None):
     """Rows of x [rows, cols] (bf16 or fp32, cols % 16 == 0) as 8-bit integers
     with one scale each: (xq [rows, cols] int8, scale [rows] fp32)."""
-    rows, cols = x.shape
-    index = _device_index(x)
-    x_st, step = x.stride()
-    if step != 1 and rows > 0 and cols > 1:
-        raise ValueError("x: each row must be contiguous")
-    if xq is None:
-        xq = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
-    elif (xq.shape != x.shape or xq.dtype is not torch.int8 or xq.get_device() != index
-          or not xq.is_contiguous()):
-        raise ValueError("xq must be contiguous int8 of x's shape")
-    if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-    _call(index, _quantize, "tg_quantize_rows", x.data_ptr(), x_st if rows > 1 else cols, rows, cols,
-          _dt(x), xq.data_ptr(), _vec(scale, rows, torch.float32, index, "scale"),
-          _stream_at(stream, index))
-    return xq, scale
+    r = _binding.quantize_rows(x, xq, scale, _handle(stream))
+    if r.__class__ is int:
+        raise TokenGateError(r, "tg_quantize_rows")
+    return r
 
 
 def tg_linear_quantized(xq, xs, wq, ws, residual=None, y=None, dtype=torch.bfloat16, stream=None):
     """y = (xq . wq^T) * xs[:, None] * ws (+ residual): xq [m, k], wq [n, k]
     int8 with their scales xs [m], ws [n] fp32 (tg_quantize_rows); y and
     residual [m, n] in dtype (bf16 or fp32)."""
-    m, k = xq.shape
-    n = wq.shape[0]
-    index = _device_index(xq)
-    i8 = torch.int8
-    if (wq.shape != (n, k) or xq.dtype is not i8 or wq.dtype is not i8 or wq.get_device() != index
-            or not xq.is_contiguous() or not wq.is_contiguous()):
-        raise ValueError("xq [m, k] and wq [n, k] must be contiguous int8 on one device")
-    if y is None:
-        y = torch.empty((m, n), dtype=dtype, device=xq.device)
-    elif y.shape != (m, n) or y.get_device() != index or not y.is_contiguous():
-        raise ValueError("y must be contiguous [m, n] on xq's device")
-    res_ptr = None
-    if residual is not None:
-        if (residual.shape != (m, n) or residual.dtype is not y.dtype
-                or residual.get_device() != index or not residual.is_contiguous()):
-            raise ValueError("residual must be contiguous [m, n], as y")
-        res_ptr = residual.data_ptr()
-    f32 = torch.float32
-    _call(index, _linear_q, "tg_linear_quantized", xq.data_ptr(), _vec(xs, m, f32, index, "xs"),
-          wq.data_ptr(), _vec(ws, n, f32, index, "ws"), res_ptr, m, n, k, _dt(y), y.data_ptr(),
-          _stream_at(stream, index))
-    return y
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise ValueError(f"unsupported dtype {dtype} (bf16 or fp32)")
+    r = _binding.linear_quantized(xq, xs, wq, ws, residual, y, dtype is torch.float32,
+                                  _handle(stream))
+    if r.__class__ is int:
+        raise TokenGateError(r, "tg_linear_quantized")
+    return r
 
 
 __all__ = [

@@ -6,6 +6,9 @@ Each .cu under csrc/ is compiled to an object under _build/ (in parallel,
 skipped when up to date), then linked into a shared library next to this
 file. The CUDA runtime is linked statically, so the library loads on a
 machine without a GPU driver (its exported symbols can be checked there).
+csrc/binding.cpp becomes the extension module _binding, which the package
+calls the library's per-token entry points through; it is built against the
+torch that runs this.
 """
 
 from __future__ import annotations
@@ -22,6 +25,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtokengate.so")
+BINDING = os.path.join(HERE, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
@@ -72,7 +76,33 @@ def build(verbose: bool = False, force: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    build_binding(verbose, force)
     return LIB
+
+
+def build_binding(verbose: bool = False, force: bool = False) -> str:
+    import sysconfig
+
+    import torch
+
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and not _newer(src, BINDING, [LIB, os.path.join(INCLUDE, "tokengate.h")]):
+        return BINDING
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-DNDEBUG",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[a for i in inc for a in ("-isystem", i)], src, "-o", BINDING,
+           "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-L" + HERE, "-l:libtokengate.so", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"binding failed:\n{r.stdout}\n{r.stderr}")
+    return BINDING
 
 
 if __name__ == "__main__":
