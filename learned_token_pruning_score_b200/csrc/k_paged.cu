@@ -13,6 +13,8 @@
 // Lengths, chunk offsets, positions and page numbers are device data: they are
 // checked where they are used, and a row or page out of range is skipped and
 // reported in the device error word.
+#include <algorithm>
+
 #include "tg_device.cuh"
 #include "tg_internal.h"
 #include "tg_paged.cuh"
@@ -223,44 +225,47 @@ __global__ void __launch_bounds__(kAppThreads, 3) paged_append(const __grid_cons
   }
 }
 
-__device__ __forceinline__ void unpack4(const uint4& u, float (&f)[4]) {
-  f[0] = __uint_as_float(u.x);
-  f[1] = __uint_as_float(u.y);
-  f[2] = __uint_as_float(u.z);
-  f[3] = __uint_as_float(u.w);
-}
-
 // ---------------------------------------------------------------- attention, CUDA cores
-// One CTA per (32 rows of a request and KV head, KV head); a row is a (token,
-// query head of the group) pair, token-major, so that the keys are read once
-// for the whole group. Keys go through shared memory 32 at a time; thread
-// (ty, tx) holds rows 2 ty, 2 ty + 1 and keys tx + 8 i in the logits, columns
-// 4 tx + 32 c in the outputs, and the running maximum and sum of its two rows
-// (equal in the eight lanes of a row). All in fp32: the fp32 block's parity
-// needs full-precision products, which no tensor-core type gives.
+// One CTA per (32 rows of a request and KV head, KV head, split of the keys); a
+// row is a (token, query head of the group) pair, token-major, so that the keys
+// are read once for the whole group. Keys go through shared memory 32 at a time,
+// the next 32 on their way (cp.async) while these are worked on; thread (ty, tx)
+// holds rows 2 ty, 2 ty + 1 and keys tx + 8 i in the logits, columns 4 tx + 32 c
+// in the outputs, and the running maximum and sum of its two rows (equal in the
+// eight lanes of a row). All in fp32: the fp32 block's parity needs
+// full-precision products, which no tensor-core type gives. Its calls are small,
+// so the keys are split until the SMs are filled (three requests of up to 130
+// tokens over up to 530 keys: 65 us unsplit and unbuffered, 25 so).
 constexpr int kSimtRows = 32, kSimtKeys = 32, kSimtThreads = 128;
 
-template <typename T, int kDh>
+template <int kDh>
 struct SimtSmem {
   float q[kSimtRows][kDh + 4];
-  float k[kSimtKeys][kDh + 4];
-  float v[kSimtKeys][kDh];
+  float k[2][kSimtKeys][kDh + 4];
+  float v[2][kSimtKeys][kDh];
   float p[kSimtRows][kSimtKeys + 1];
-  float bias[kSimtKeys];
+  float bias[2][kSimtKeys];
 };
 
-template <typename T, int kDh>
+// 16 bytes global -> shared, zeros where `there` is false
+__device__ __forceinline__ void cp_async16(float* dst, const float* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+
+template <int kDh>
 __global__ void __launch_bounds__(kSimtThreads)
     paged_attn_simt(const __grid_constant__ PagedAttnArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  SimtSmem<T, kDh>& sm = *reinterpret_cast<SimtSmem<T, kDh>*>(smem_raw);
+  SimtSmem<kDh>& sm = *reinterpret_cast<SimtSmem<kDh>*>(smem_raw);
   __shared__ PagedTile s_tile;
   pdl_trigger();
   pdl_wait();
-  constexpr int kVec = 16 / static_cast<int>(sizeof(T));
   constexpr int kCols = kDh / 32;  // float4 columns of a thread's outputs
+  constexpr int kUnits = kDh / 4;  // 16-byte units of a row
   const int group = a.hq / a.kv.hkv;
-  const int g = blockIdx.y;
+  const int g = blockIdx.y, split = blockIdx.z;
   if (threadIdx.x < 32) {
     const PagedTile t = find_tile(a, kSimtRows, static_cast<int>(blockIdx.x));
     if (threadIdx.x == 0) s_tile = t;
@@ -269,34 +274,55 @@ __global__ void __launch_bounds__(kSimtThreads)
   const PagedTile tile = s_tile;
   if (tile.req < 0) return;
   const int tid = threadIdx.x, tx = tid & 7, ty = tid >> 3;
-  // rows of the tile: token (row0 + r) / group of the request, head (row0 + r) % group
   const int n_rows = min(kSimtRows, tile.n * group - tile.row0);
-  for (int e = tid; e < kSimtRows * (kDh / kVec); e += kSimtThreads) {
-    const int r = e / (kDh / kVec), c = (e % (kDh / kVec)) * kVec;
-    float f[kVec];
-    uint4 u = make_uint4(0, 0, 0, 0);
+  const int64_t lo64 = split * a.chunk;
+  const int max_limit = tile.past + (tile.row0 + n_rows - 1) / group + 1;  // the last row's limit
+  const int kv_end = static_cast<int>(min(static_cast<int64_t>(max_limit), lo64 + a.chunk));
+  const int lo = static_cast<int>(min(lo64, static_cast<int64_t>(0x7FFFFFFF)));
+  auto load = [&](int kv0, int st) {
+#pragma unroll
+    for (int i = 0; i < kSimtKeys * kUnits / kSimtThreads; ++i) {
+      const int e = tid + i * kSimtThreads;
+      const int r = e / kUnits, c = (e % kUnits) * 4;
+      const int j = kv0 + r;
+      const int64_t page = j < kv_end ? page_of(a, tile.req, j) : -1;
+      const int in = row_in_page(a, j);
+      const int64_t off = (static_cast<int64_t>(in) * a.kv.hkv + g) * kDh + c;
+      const bool there = page >= 0;
+      const float* kp = static_cast<const float*>(a.kv.k);
+      const float* vp = static_cast<const float*>(a.kv.v);
+      cp_async16(&sm.k[st][r][c], there ? kp + page * a.kv.k_page_stride + off : kp, there);
+      cp_async16(&sm.v[st][r][c], there ? vp + page * a.kv.v_page_stride + off : vp, there);
+      if (c == 0)
+        sm.bias[st][r] =
+            there && a.kv.bias ? key_bias(__ldg(a.kv.bias + page * a.kv.bias_page_stride + in)) : 0.f;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (lo < kv_end) load(lo, 0);
+  for (int e = tid; e < kSimtRows * kUnits; e += kSimtThreads) {
+    const int r = e / kUnits, c = (e % kUnits) * 4;
+    float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < n_rows) {
       const int rr = tile.row0 + r;
-      u = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
-                                          static_cast<int64_t>(tile.tok0 + rr / group) * a.q_stride +
-                                          (g * group + rr % group) * kDh + c);
+      u = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
+                                           static_cast<int64_t>(tile.tok0 + rr / group) * a.q_stride +
+                                           (g * group + rr % group) * kDh + c);
     }
-    unpack4(u, f);
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) sm.q[r][c + i] = f[i];
+    *reinterpret_cast<float4*>(&sm.q[r][c]) = u;
   }
   float scale[2], gain[2];
   int limit[2];  // keys that the row sees
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = 2 * ty + i;
+    const bool on = r < n_rows;
     const int rr = tile.row0 + r;
     const int h = g * group + rr % group;
-    scale[i] = kLog2e / (sqrtf(static_cast<float>(kDh)) * (a.tau ? __ldg(a.tau + h) : 1.0f));
-    gain[i] = a.gain && a.kv.bias ? __ldg(a.gain + h) * kLog2e : 0.0f;
-    limit[i] = r < n_rows ? tile.past + rr / group + 1 : 0;
+    scale[i] = kLog2e / (sqrtf(static_cast<float>(kDh)) * (a.tau && on ? __ldg(a.tau + h) : 1.0f));
+    gain[i] = a.gain && a.kv.bias && on ? __ldg(a.gain + h) * kLog2e : 0.0f;
+    limit[i] = on ? tile.past + rr / group + 1 : 0;
   }
-  const int kv_end = tile.past + (tile.row0 + n_rows - 1) / group + 1;  // last row's limit
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   float4 o[2][kCols];
 #pragma unroll
@@ -304,36 +330,12 @@ __global__ void __launch_bounds__(kSimtThreads)
 #pragma unroll
     for (int c = 0; c < kCols; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
 
-  for (int kv0 = 0; kv0 < kv_end; kv0 += kSimtKeys) {
-    __syncthreads();  // the last tile's keys are read
-    for (int e = tid; e < kSimtKeys * (kDh / kVec); e += kSimtThreads) {
-      const int r = e / (kDh / kVec), c = (e % (kDh / kVec)) * kVec;
-      const int j = kv0 + r;
-      float fk[kVec], fv[kVec];
-      uint4 uk = make_uint4(0, 0, 0, 0), uv = uk;
-      float b = 0.f;
-      if (j < kv_end) {
-        const int64_t page = page_of(a, tile.req, j);
-        if (page >= 0) {
-          const int64_t off = (static_cast<int64_t>(row_in_page(a, j)) * a.kv.hkv + g) * kDh + c;
-          uk = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.kv.k) +
-                                               page * a.kv.k_page_stride + off);
-          uv = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.kv.v) +
-                                               page * a.kv.v_page_stride + off);
-          if (c == 0 && a.kv.bias)
-            b = key_bias(a.kv.bias[page * a.kv.bias_page_stride + row_in_page(a, j)]);
-        }
-      }
-      unpack4(uk, fk);
-      unpack4(uv, fv);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        sm.k[r][c + i] = fk[i];
-        sm.v[r][c + i] = fv[i];
-      }
-      if (c == 0) sm.bias[r] = b;
-    }
-    __syncthreads();
+  int st = 0;
+  for (int kv0 = lo; kv0 < kv_end; kv0 += kSimtKeys, st ^= 1) {
+    if (kv0 + kSimtKeys < kv_end) load(kv0 + kSimtKeys, st ^ 1);
+    else asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();  // this stage's keys are there for every thread
     float s[2][4] = {};
 #pragma unroll 4
     for (int d = 0; d < kDh; d += 4) {
@@ -341,18 +343,23 @@ __global__ void __launch_bounds__(kSimtThreads)
       const float4 q1 = *reinterpret_cast<const float4*>(&sm.q[2 * ty + 1][d]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float4 kk = *reinterpret_cast<const float4*>(&sm.k[tx + 8 * i][d]);
+        const float4 kk = *reinterpret_cast<const float4*>(&sm.k[st][tx + 8 * i][d]);
         s[0][i] += q0.x * kk.x + q0.y * kk.y + q0.z * kk.z + q0.w * kk.w;
         s[1][i] += q1.x * kk.x + q1.y * kk.y + q1.z * kk.z + q1.w * kk.w;
       }
     }
+    bool all = true;  // every key of the stage is seen by both rows
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       float mx = -INFINITY;
+      bool seen[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float z = s[r][i] * scale[r] + gain[r] * sm.bias[tx + 8 * i];
-        s[r][i] = kv0 + tx + 8 * i < limit[r] && !(z <= kMaskedLogit) ? z : -INFINITY;
+        const int j = kv0 + tx + 8 * i;
+        const float z = s[r][i] * scale[r] + gain[r] * sm.bias[st][tx + 8 * i];
+        seen[i] = j < limit[r] && j < kv_end && !(z <= kMaskedLogit);
+        all = all && seen[i];
+        s[r][i] = seen[i] ? z : -INFINITY;
         mx = fmaxf(mx, s[r][i]);
       }
 #pragma unroll
@@ -363,9 +370,8 @@ __global__ void __launch_bounds__(kSimtThreads)
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const bool seen = kv0 + tx + 8 * i < limit[r] && !(s[r][i] == -INFINITY);
         const float w = exp2f(s[r][i] - m_use);
-        sm.p[2 * ty + r][tx + 8 * i] = seen ? w : -1.0f;
+        sm.p[2 * ty + r][tx + 8 * i] = seen[i] ? w : -1.0f;
         sum += w;
       }
 #pragma unroll
@@ -380,30 +386,41 @@ __global__ void __launch_bounds__(kSimtThreads)
         o[r][c].w *= corr;
       }
     }
-    __syncwarp();  // a row's weights are written and read by one warp
-    // keys that a row does not see (weight -1) are skipped, not weighted with
-    // zero: their values may be infinite or NaN
-#pragma unroll 2
-    for (int j = 0; j < kSimtKeys; ++j) {
-      const float p0 = sm.p[2 * ty][j], p1 = sm.p[2 * ty + 1][j];
-      const bool see0 = !(p0 < 0.f), see1 = !(p1 < 0.f);
+    // (also: a row's weights are written and read by one warp)
+    all = __all_sync(0xFFFFFFFFu, all);
+    __syncwarp();
+    auto add = [&](float4& acc, float p, const float4& vv) {
+      acc.x = fmaf(p, vv.x, acc.x);
+      acc.y = fmaf(p, vv.y, acc.y);
+      acc.z = fmaf(p, vv.z, acc.z);
+      acc.w = fmaf(p, vv.w, acc.w);
+    };
+    if (all) {
+#pragma unroll 4
+      for (int j = 0; j < kSimtKeys; ++j) {
+        const float p0 = sm.p[2 * ty][j], p1 = sm.p[2 * ty + 1][j];
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        const float4 vv = *reinterpret_cast<const float4*>(&sm.v[j][4 * tx + 32 * c]);
-        if (see0) {
-          o[0][c].x = fmaf(p0, vv.x, o[0][c].x);
-          o[0][c].y = fmaf(p0, vv.y, o[0][c].y);
-          o[0][c].z = fmaf(p0, vv.z, o[0][c].z);
-          o[0][c].w = fmaf(p0, vv.w, o[0][c].w);
+        for (int c = 0; c < kCols; ++c) {
+          const float4 vv = *reinterpret_cast<const float4*>(&sm.v[st][j][4 * tx + 32 * c]);
+          add(o[0][c], p0, vv);
+          add(o[1][c], p1, vv);
         }
-        if (see1) {
-          o[1][c].x = fmaf(p1, vv.x, o[1][c].x);
-          o[1][c].y = fmaf(p1, vv.y, o[1][c].y);
-          o[1][c].z = fmaf(p1, vv.z, o[1][c].z);
-          o[1][c].w = fmaf(p1, vv.w, o[1][c].w);
+      }
+    } else {
+      // keys that a row does not see (weight -1) are skipped, not weighted with
+      // zero: their values may be infinite or NaN
+#pragma unroll 1
+      for (int j = 0; j < kSimtKeys; ++j) {
+        const float p0 = sm.p[2 * ty][j], p1 = sm.p[2 * ty + 1][j];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          const float4 vv = *reinterpret_cast<const float4*>(&sm.v[st][j][4 * tx + 32 * c]);
+          if (!(p0 < 0.f)) add(o[0][c], p0, vv);
+          if (!(p1 < 0.f)) add(o[1][c], p1, vv);
         }
       }
     }
+    __syncthreads();  // the stage is read: the next load but one may fill it
   }
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
@@ -411,21 +428,19 @@ __global__ void __launch_bounds__(kSimtThreads)
     const int rr = tile.row0 + 2 * ty + r;
     const int64_t t = tile.tok0 + rr / group;
     const int h = g * group + rr % group;
+    const bool part = a.splits > 1;
     const bool any = l[r] != 0.f;  // a row that sees nothing is zero
-    const float inv = any ? 1.0f / l[r] : 0.f;
-    if (a.lse != nullptr && tx == 0)
-      a.lse[h * a.rows + t] = any ? (m[r] + log2f(l[r])) * kLn2 : -INFINITY;
-    T* out = static_cast<T*>(a.out) + (t * a.hq + h) * kDh;
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) {
-      const float f[4] = {o[r][c].x * inv, o[r][c].y * inv, o[r][c].z * inv, o[r][c].w * inv};
-      if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4*>(out + 4 * tx + 32 * c) = make_float4(f[0], f[1], f[2], f[3]);
-      } else {
-        *reinterpret_cast<uint2*>(out + 4 * tx + 32 * c) =
-            make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-      }
+    const float inv = part ? 1.0f : any ? 1.0f / l[r] : 0.f;
+    const int64_t at = (part ? split * a.rows * a.hq : 0) + t * a.hq + h;
+    if (tx == 0) {
+      if (part) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(m[r], l[r]);
+      else if (a.lse != nullptr) a.lse[h * a.rows + t] = any ? (m[r] + log2f(l[r])) * kLn2 : -INFINITY;
     }
+    float* out = (part ? a.part_o : static_cast<float*>(a.out)) + at * kDh;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c)
+      *reinterpret_cast<float4*>(out + 4 * tx + 32 * c) =
+          make_float4(o[r][c].x * inv, o[r][c].y * inv, o[r][c].z * inv, o[r][c].w * inv);
   }
 }
 
@@ -439,15 +454,15 @@ cudaError_t run_append(const PagedAppendArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename T, int kDh>
+template <int kDh>
 cudaError_t run_simt(const PagedAttnArgs& a, cudaStream_t st) {
-  const int64_t tiles = paged_row_tiles(a.rows, a.batch, a.hq, a.kv.hkv, kSimtRows);
-  constexpr int kBytes = static_cast<int>(sizeof(SimtSmem<T, kDh>));
-  auto kern = paged_attn_simt<T, kDh>;
+  constexpr int kBytes = static_cast<int>(sizeof(SimtSmem<kDh>));
+  auto kern = paged_attn_simt<kDh>;
   TG_CUDA_TRY(set_smem_attr_once(reinterpret_cast<const void*>(kern), kBytes));
-  TG_CUDA_TRY(launch_pdl(kern, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.kv.hkv)),
-                         dim3(kSimtThreads), kBytes, st, a));
-  return cudaGetLastError();
+  return launch_pdl(kern,
+                    dim3(static_cast<unsigned>(a.tiles), static_cast<unsigned>(a.kv.hkv),
+                         static_cast<unsigned>(a.splits)),
+                    dim3(kSimtThreads), kBytes, st, a);
 }
 
 }  // namespace
@@ -459,8 +474,19 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, bool bf16, cudaStream_
   return a.kv.dh == 128 ? run_append<float, 128>(a, st) : run_append<float, 64>(a, st);
 }
 
-cudaError_t launch_paged_attn_simt(const PagedAttnArgs& a, cudaStream_t st) {
-  return a.kv.dh == 128 ? run_simt<float, 128>(a, st) : run_simt<float, 64>(a, st);
+cudaError_t launch_paged_attn_simt(PagedAttnArgs a, void* ws, cudaStream_t st) {
+  a.tiles = paged_row_tiles(a.rows, a.batch, a.hq, a.kv.hkv, kSimtRows);
+  // splits of 64 keys at least, until every SM has three CTAs
+  const int64_t jobs = a.tiles * a.kv.hkv;
+  const int64_t most = std::min<int64_t>(paged_max_splits(a.rows, a.hq, a.kv.dh), 3 * num_sms() / jobs);
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(most, a.max_kv / 64));
+  a.chunk = ((a.max_kv + want - 1) / want + kSimtKeys - 1) / kSimtKeys * kSimtKeys;
+  a.chunk0 = a.chunk;
+  a.splits = static_cast<int>((a.max_kv + a.chunk - 1) / a.chunk);
+  paged_partials(&a, ws);
+  const cudaError_t e = a.kv.dh == 128 ? run_simt<128>(a, st) : run_simt<64>(a, st);
+  if (e != cudaSuccess || a.splits == 1) return e;
+  return launch_paged_merge(a, false, st);
 }
 
 }  // namespace tg

@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 // warps' sums are added in order. A split without keys for the row has sum 0
 // and its output is not read. One warp a row where there are few splits; with
 // many of them (few rows then) eight, so that they arrive together.
-template <int kDh, int kWarps>
+template <typename T, int kDh, int kWarps>
 __global__ void __launch_bounds__(256) paged_merge(const __grid_constant__ PagedAttnArgs a) {
   __shared__ float s_acc[kWarps > 1 ? kWarps : 1][kDh];
   pdl_trigger();
@@ -558,19 +558,23 @@ __global__ void __launch_bounds__(256) paged_merge(const __grid_constant__ Paged
   const float inv = any ? 1.0f / sum : 0.f;
   if (lane == 0 && a.lse != nullptr)
     a.lse[h * a.rows + t] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) +
-                                              static_cast<int64_t>(idx) * kDh + lane * kN);
+  T* out = static_cast<T*>(a.out) + static_cast<int64_t>(idx) * kDh + lane * kN;
 #pragma unroll
-  for (int e = 0; e < kN / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  for (int e = 0; e < kN; e += 2) {
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float2*>(out + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
+    else
+      *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  }
 }
 
-template <int kDh>
+template <typename T, int kDh>
 cudaError_t merge(const PagedAttnArgs& a, cudaStream_t st) {
   const int64_t n = a.rows * a.hq;
   // (4096 keys in 33 splits, 16 rows: 13.1 us with one warp, 4.7 with eight)
   if (a.splits <= 2 || (a.splits <= 8 && n > 16 * num_sms()))
-    return launch_pdl(paged_merge<kDh, 1>, dim3(static_cast<unsigned>((n + 7) / 8)), dim3(256), 0, st, a);
-  return launch_pdl(paged_merge<kDh, 8>, dim3(static_cast<unsigned>(n)), dim3(256), 0, st, a);
+    return launch_pdl(paged_merge<T, kDh, 1>, dim3(static_cast<unsigned>((n + 7) / 8)), dim3(256), 0, st, a);
+  return launch_pdl(paged_merge<T, kDh, 8>, dim3(static_cast<unsigned>(n)), dim3(256), 0, st, a);
 }
 
 template <int kDh>
@@ -609,8 +613,9 @@ cudaError_t run(const PagedAttnArgs& a, int64_t tiles, bool cluster, cudaStream_
 
 }  // namespace
 
-cudaError_t launch_paged_merge(const PagedAttnArgs& a, cudaStream_t st) {
-  return a.kv.dh == 128 ? merge<128>(a, st) : merge<64>(a, st);
+cudaError_t launch_paged_merge(const PagedAttnArgs& a, bool bf16, cudaStream_t st) {
+  if (bf16) return a.kv.dh == 128 ? merge<__nv_bfloat16, 128>(a, st) : merge<__nv_bfloat16, 64>(a, st);
+  return a.kv.dh == 128 ? merge<float, 128>(a, st) : merge<float, 64>(a, st);
 }
 
 cudaError_t launch_paged_decode(PagedAttnArgs a, void* ws, cudaStream_t st) {
@@ -644,7 +649,7 @@ cudaError_t launch_paged_decode(PagedAttnArgs a, void* ws, cudaStream_t st) {
   paged_partials(&a, ws);
   const cudaError_t e = a.kv.dh == 128 ? run<128>(a, tiles, false, st) : run<64>(a, tiles, false, st);
   if (e != cudaSuccess || a.splits == 1) return e;
-  return launch_paged_merge(a, st);
+  return launch_paged_merge(a, true, st);
 }
 
 }  // namespace tg

@@ -794,7 +794,7 @@ cudaError_t launch_paged_tc(PagedAttnArgs a, void* ws, cudaStream_t st) {
   if (a.kv.dh == 128) e = bias ? run<128, true>(a, st) : run<128, false>(a, st);
   else e = bias ? run<64, true>(a, st) : run<64, false>(a, st);
   if (e != cudaSuccess || a.splits == 1) return e;
-  return launch_paged_merge(a, st);
+  return launch_paged_merge(a, true, st);
 }
 
 }  // namespace tg

@@ -18,6 +18,7 @@
 //           through every SM; the partial sums meet through distributed shared
 //           memory. Bound by HBM (each weight read once).
 #include <atomic>
+#include <type_traits>
 
 #include "tg_device.cuh"
 #include "tg_internal.h"
@@ -314,7 +315,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // stores every cluster-size-th group of columns.
 struct Narrow {
   static constexpr int kWBytes = 128 * kBK;
-  static constexpr int kRing = 96 * 1024;  // two CTAs on an SM
+  // two CTAs on an SM, of one call or of one and the next
+  static constexpr int kRing = 96 * 1024;
   static constexpr int kMaxCols = 128;
   static constexpr int kMaxStages = 5;
   static constexpr size_t kSmem = 1024 + kRing + 256;
@@ -370,6 +372,29 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
+  // What the end needs besides the sums is read now: the scales of this lane's
+  // four channels, and for the warp's first two columns (part 8 + warp, then
+  // split 8 on) the row's scale and the residual.
+  const int cols = static_cast<int>(min(static_cast<int64_t>(p.cols), p.m - x_row));
+  const int ch = w_row + lane * 4;
+  const int c_first = part * 8 + warp, c_step = split * 8;
+  const bool ch_ok = ch < p.n;
+  using Quad = typename std::conditional<sizeof(T) == 4, uint4, uint2>::type;  // four outputs
+  float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+  float xs[2];
+  Quad res[2];
+  auto column = [&](int c, float& x, Quad& r) {
+    x = 0.f;
+    r = Quad{};
+    if (ch_ok && c < cols) {
+      x = __ldg(p.xs + x_row + c);
+      if (p.residual != nullptr)
+        r = *reinterpret_cast<const Quad*>(static_cast<const T*>(p.residual) + (x_row + c) * p.n + ch);
+    }
+  };
+  if (ch_ok) w = __ldg(reinterpret_cast<const float4*>(p.ws + ch));
+  column(c_first, xs[0], res[0]);
+  column(c_first + c_step, xs[1], res[1]);
   if (warp == 0 && lane == 0) {
     int s = 0;
     uint32_t ph = 0;
@@ -424,47 +449,47 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (split > 1) cluster_sync();
   else __syncthreads();
   tc_fence_after();
-  const int cols = static_cast<int>(min(static_cast<int64_t>(p.cols), p.m - x_row));
-  if (s_bad == 0) {
-    // one warp per column: lane's four channels, one after the other part's sums
-    const int ch = w_row + lane * 4;
-    if (ch < p.n) {
-      const float4 w = __ldg(reinterpret_cast<const float4*>(p.ws + ch));
-      for (int c = part * 8 + warp; c < cols; c += split * 8) {
-        const uint32_t at = smem_addr(sums + c * 128 + lane * 4);
-        int4 a = make_int4(0, 0, 0, 0);
-        if (split > 1) {
-          for (int q = 0; q < split; ++q) {
-            const int4 b = ld_cluster_int4(mapa_shared(at, static_cast<uint32_t>(q)));
-            a.x += b.x;
-            a.y += b.y;
-            a.z += b.z;
-            a.w += b.w;
-          }
-        } else {
-          a = *reinterpret_cast<const int4*>(sums + c * 128 + lane * 4);
+  if (s_bad == 0 && ch_ok) {
+    // one warp per column: lane's four channels, the parts' sums in their order
+#pragma unroll 1
+    for (int c = c_first, k = 0; c < cols; c += c_step, ++k) {
+      if (k >= 2) column(c, xs[0], res[0]);
+      const float x = k == 1 ? xs[1] : xs[0];
+      const Quad r = k == 1 ? res[1] : res[0];
+      const uint32_t at = smem_addr(sums + c * 128 + lane * 4);
+      int4 a = make_int4(0, 0, 0, 0);
+      if (split > 1) {
+        int4 b[8];  // all on their way before the first is added
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          b[q] = q < split ? ld_cluster_int4(mapa_shared(at, static_cast<uint32_t>(q)))
+                           : make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          a.x += b[q].x;
+          a.y += b[q].y;
+          a.z += b[q].z;
+          a.w += b[q].w;
         }
-        const float xs = __ldg(p.xs + x_row + c);
-        float4 v = make_float4(static_cast<float>(a.x) * xs * w.x, static_cast<float>(a.y) * xs * w.y,
-                               static_cast<float>(a.z) * xs * w.z, static_cast<float>(a.w) * xs * w.w);
-        const int64_t yi = (x_row + c) * p.n + ch;
-        if constexpr (sizeof(T) == 4) {
-          if (p.residual != nullptr) {
-            const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + yi);
-            v = make_float4(v.x + r.x, v.y + r.y, v.z + r.z, v.w + r.w);
-          }
-          *reinterpret_cast<float4*>(static_cast<float*>(p.y) + yi) = v;
-        } else {
-          if (p.residual != nullptr) {
-            const uint2 u =
-                *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.residual) + yi);
-            const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-            const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-            v = make_float4(v.x + lo.x, v.y + lo.y, v.z + hi.x, v.w + hi.y);
-          }
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + yi) =
-              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      } else {
+        a = *reinterpret_cast<const int4*>(sums + c * 128 + lane * 4);
+      }
+      float4 v = make_float4(static_cast<float>(a.x) * x * w.x, static_cast<float>(a.y) * x * w.y,
+                             static_cast<float>(a.z) * x * w.z, static_cast<float>(a.w) * x * w.w);
+      T* y = static_cast<T*>(p.y) + (x_row + c) * p.n + ch;
+      const bool add = p.residual != nullptr;
+      if constexpr (sizeof(T) == 4) {
+        if (add)
+          v = make_float4(v.x + __uint_as_float(r.x), v.y + __uint_as_float(r.y),
+                          v.z + __uint_as_float(r.z), v.w + __uint_as_float(r.w));
+        *reinterpret_cast<float4*>(y) = v;
+      } else {
+        if (add) {
+          const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.x));
+          const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.y));
+          v = make_float4(v.x + lo.x, v.y + lo.y, v.z + hi.x, v.w + hi.y);
         }
+        *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
       }
     }
   }
@@ -529,19 +554,20 @@ cudaError_t run_narrow(const QuantGemmArgs& g, cudaStream_t st) {
   p.residual = g.residual;
   p.y = g.y;
   p.cols = g.m >= C::kMaxCols ? C::kMaxCols : static_cast<int>((g.m + 15) / 16 * 16);
-  p.stages = C::kRing / (C::kWBytes + p.cols * kBK);
-  if (p.stages > C::kMaxStages) p.stages = C::kMaxStages;
   p.err = device_error_word();
   CUtensorMap tx, tw;
   if (!make_tmap_2d_u8(&tx, g.x, g.m, g.k, p.cols) || !make_tmap_2d_u8(&tw, g.w, g.n, g.k, 128))
     return cudaErrorInvalidValue;
   const int tiles_n = (g.n + 127) / 128;
   const int tiles_m = static_cast<int>((g.m + C::kMaxCols - 1) / C::kMaxCols);
-  // k is split until the CTAs fill the SMs (two fit on one), each keeping two
-  // stages of k at least.
+  // k is split until the next doubling would pass one CTA an SM, each CTA keeping
+  // two stages of k at least (64 x 4096 x 2048: 4 parts, 128 CTAs, 7.2 us, 8 parts
+  // 7.9; 128 x 12288 x 2048: 1 part, 96 CTAs, 14.5 us, 2 parts 15.6).
   const int num_kb = (g.k + kBK - 1) / kBK;
   int split = 1;
-  while (split < 8 && tiles_n * tiles_m * split * 2 <= 2 * num_sms() && num_kb >= 4 * split) split *= 2;
+  while (split < 8 && tiles_n * tiles_m * split * 2 <= num_sms() && num_kb >= 4 * split) split *= 2;
+  p.stages = C::kRing / (C::kWBytes + p.cols * kBK);
+  if (p.stages > C::kMaxStages) p.stages = C::kMaxStages;
   auto kern = gemm_i8_narrow<T>;
   TG_CUDA_TRY(set_smem_attr_once(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmem)));
   cudaLaunchConfig_t cfg = {};

@@ -974,7 +974,7 @@ size_t tg_workspace_size(tg_op op, const tg_shape* s) {
       return DecodePlan(nullptr, m, s->k).bytes;
     }
     case TG_OP_PAGED_ATTN:
-      if (s->dtype != TG_BF16 || s->k < 1 || s->n < 1 || s->n_heads_kv < 1 || s->head_dim < 1 ||
+      if (s->k < 1 || s->n < 1 || s->n_heads_kv < 1 || s->head_dim < 1 ||
           s->n_heads_q < s->n_heads_kv)
         return 0;
       return paged_attn_ws_bytes(s->k, s->n_heads_q, s->head_dim);
@@ -2059,15 +2059,12 @@ tg_status tg_paged_attn(const tg_paged_kv* cache, const void* q, int64_t q_strid
   a.out = out;
   a.lse = lse;
   a.err = device_error_word();
-  if (dt == TG_BF16) {
-    TG_CHECK(ws != nullptr && ws_bytes >= paged_attn_ws_bytes(rows, hq, dh),
-             TG_ERR_WORKSPACE);
-    TG_CHECK(aligned16(ws), TG_ERR_INVALID_ARG);
-  }
+  TG_CHECK(ws != nullptr && ws_bytes >= paged_attn_ws_bytes(rows, hq, dh), TG_ERR_WORKSPACE);
+  TG_CHECK(aligned16(ws), TG_ERR_INVALID_ARG);
   const double bytes = 2.0 * rows * hq * dh * double(elem_size(dt));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return cuda_status(traced(TG_K_PAGED_ATTN, rows, 0.0, bytes, st, [&] {
-    if (dt == TG_F32) return launch_paged_attn_simt(a, st);
+    if (dt == TG_F32) return launch_paged_attn_simt(a, ws, st);
     return paged_tile_rows(rows, batch, hq, hkv) == 16 ? launch_paged_decode(a, ws, st)
                                                        : launch_paged_tc(a, ws, st);
   }));

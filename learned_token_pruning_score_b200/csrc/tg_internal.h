@@ -385,7 +385,7 @@ struct PagedAttnArgs {
   void* out;                        // [rows, hq, dh]
   float* lse;                       // [hq, rows] or null
   unsigned int* err;
-  // bf16: the keys are split, [0, chunk0), then pieces of `chunk`
+  // The keys are split: [0, chunk0), then pieces of `chunk`.
   int splits;
   int64_t chunk0, chunk;
   int64_t tiles;                    // row tiles of the launch (upper bound)
@@ -417,12 +417,12 @@ inline void paged_partials(PagedAttnArgs* a, void* ws) {
   a->part_ml = a->part_o + n * a->kv.dh;
 }
 // fp32, CUDA cores (k_paged.cu)
-cudaError_t launch_paged_attn_simt(const PagedAttnArgs& a, cudaStream_t st);
+cudaError_t launch_paged_attn_simt(PagedAttnArgs a, void* ws, cudaStream_t st);
 // bf16: few rows a request (k_paged_decode.cu)
 cudaError_t launch_paged_decode(PagedAttnArgs a, void* ws, cudaStream_t st);
 // bf16: chunks (k_paged_tc.cu)
 cudaError_t launch_paged_tc(PagedAttnArgs a, void* ws, cudaStream_t st);
-cudaError_t launch_paged_merge(const PagedAttnArgs& a, cudaStream_t st);
+cudaError_t launch_paged_merge(const PagedAttnArgs& a, bool bf16, cudaStream_t st);
 
 // ---- 8-bit integers (k_quant.cu)
 // xq = rint(127 x / amax), scale = amax / 127 per row; cols % 16 == 0.
