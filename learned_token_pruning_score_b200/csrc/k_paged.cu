@@ -51,12 +51,41 @@ __device__ __forceinline__ uint4 repack2(const float2 (&f)[2]) {
 // second, so that rotation pairs meet in one thread and the norm needs three
 // shuffles. A CTA takes `tok` tokens: their angles (fp64, from the host's
 // theta_i, so that no thread evaluates a power) go to shared memory first.
-// The loads of a CTA's tokens are on their way while pages and angles are found.
+// CTAs run through groups of `tok` tokens: while one group is worked on, the next
+// one's vectors are on their way to shared memory (cp.async; each thread reads
+// back what it fetched itself) and its angles are formed, and a ninth warp finds
+// the pages of the one after that. (Loads into registers instead, a group a CTA:
+// 113 us for 32768 tokens; so 101.)
 constexpr int kAppThreads = 256, kAppTok = 4;
 
+// 16 bytes global -> shared
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+
 template <typename T, int kDh>
-__global__ void __launch_bounds__(kAppThreads, 3) paged_append(const __grid_constant__ PagedAppendArgs a,
-                                                               int tok) {
+struct AppSmem {
+  uint4 ring[2][kAppTok][2][kAppThreads];  // halves of a head's row, by thread
+  // by quads of a thread's frequencies (app_at): lanes read side by side
+  float cos[2][kAppTok][kDh / 2], sin[2][kAppTok][kDh / 2];
+  float norm[2][2][kDh / 2];               // weights of q and k (read as they are aligned), halves
+  int64_t page[3][kAppTok];                // page of the token's row, or -1 (skip)
+  int64_t pos[3][kAppTok];
+  int row[3][kAppTok];
+};
+// Place of frequency f, of which a thread has kVec in a row.
+template <int kDh, int kVec>
+__device__ __forceinline__ int app_at(int f) {
+  constexpr int kLanes = kDh / 2 / kVec;
+  const int sub = f / kVec, e = f % kVec;
+  return (e >> 2) * (kLanes * 4) + sub * 4 + (e & 3);
+}
+
+template <typename T, int kDh>
+__global__ void __launch_bounds__(kAppThreads + 32, 3)
+    paged_append(const __grid_constant__ PagedAppendArgs a, int tok) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  AppSmem<T, kDh>& sm = *reinterpret_cast<AppSmem<T, kDh>*>(smem_raw);
   pdl_trigger();
   pdl_wait();
   constexpr int kHalf = kDh / 2;
@@ -64,164 +93,226 @@ __global__ void __launch_bounds__(kAppThreads, 3) paged_append(const __grid_cons
   constexpr int kPairs = kVec / 2;
   constexpr int kLanes = kHalf / kVec;           // lanes of one head
   constexpr int kHeads = kAppThreads / kLanes;   // heads of one pass
-  __shared__ __align__(16) float s_cos[kAppTok][kHalf];
-  __shared__ __align__(16) float s_sin[kAppTok][kHalf];
-  __shared__ __align__(16) float s_norm[2][kDh];  // weights of q and k (read as they are aligned)
-  __shared__ int64_t s_dst_page[kAppTok];  // page of the token's row, or -1 (skip)
-  __shared__ int s_dst_row[kAppTok];
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tok;
-  const int nt = static_cast<int>(min(static_cast<int64_t>(tok), a.rows - t0));
-  const int lane = threadIdx.x & 31;
-  // request of each token: the number of requests that end at or before it
-  // (cu_q ascends), counted by every warp
-  int req[kAppTok] = {};
-  for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const int64_t end = b0 + lane < a.batch ? __ldg(a.cu_q + b0 + lane + 1) : int64_t(1) << 62;
-#pragma unroll
-    for (int i = 0; i < kAppTok; ++i) req[i] += __popc(__ballot_sync(0xFFFFFFFFu, end <= t0 + i));
-  }
-  const int sub = threadIdx.x % kLanes;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const bool finder = tid >= kAppThreads;        // the ninth warp
+  const int64_t groups = (a.rows + tok - 1) / tok;
+  // rows from cu_q[batch] on belong to no request: neither read nor written
+  const int64_t total = min(a.rows, static_cast<int64_t>(__ldg(a.cu_q + a.batch)));
+  const int sub = tid % kLanes, d0 = sub * kVec;
   const int heads = a.hq + 2 * a.kv.hkv;
-  const int d0 = sub * kVec;
-  // head h0 of token t: q, k and v in turn; rows of no request are not read
-  uint4 ulo[kAppTok], uhi[kAppTok];
-  auto load = [&](int h0) {
-    const T* src = nullptr;
-    int64_t stride = 0;
+  // head h0's row of token 0: q, k and v in turn
+  auto source = [&](int h0, int64_t& stride) -> const T* {
     if (h0 < a.hq) {
-      src = static_cast<const T*>(a.q) + h0 * kDh;
       stride = a.q_stride;
-    } else if (h0 < a.hq + a.kv.hkv) {
-      src = static_cast<const T*>(a.k) + (h0 - a.hq) * kDh;
-      stride = a.k_stride;
-    } else if (h0 < heads) {
-      src = static_cast<const T*>(a.v) + (h0 - a.hq - a.kv.hkv) * kDh;
-      stride = a.v_stride;
+      return static_cast<const T*>(a.q) + h0 * kDh + d0;
     }
-    src += t0 * stride + d0;
+    h0 -= a.hq;
+    if (h0 < a.kv.hkv) {
+      stride = a.k_stride;
+      return static_cast<const T*>(a.k) + h0 * kDh + d0;
+    }
+    stride = a.v_stride;
+    return static_cast<const T*>(a.v) + (h0 - a.kv.hkv) * kDh + d0;
+  };
+  int64_t stride0 = 0;
+  const T* src0 = !finder && tid / kLanes < heads ? source(tid / kLanes, stride0) : nullptr;
+  auto fetch = [&](int64_t group, int st) {
 #pragma unroll
     for (int i = 0; i < kAppTok; ++i) {
-      ulo[i] = uhi[i] = make_uint4(0, 0, 0, 0);
-      if (i < nt && h0 < heads && req[i] < a.batch) {
-        ulo[i] = *reinterpret_cast<const uint4*>(src + i * stride);
-        uhi[i] = *reinterpret_cast<const uint4*>(src + i * stride + kHalf);
+      const int64_t t = group * tok + i;
+      if (i < tok && t < total && src0 != nullptr) {
+        cp_async16(&sm.ring[st][i][0][tid], src0 + t * stride0);
+        cp_async16(&sm.ring[st][i][1][tid], src0 + t * stride0 + kHalf);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // pages, rows, positions and gate biases of a group; lane i has token i
+  auto find = [&](int64_t group, int st) {
+    const int64_t t = group * tok + lane;
+    const bool on = lane < tok && t < total;
+    int64_t pos = on && a.rotate && a.pos != nullptr ? __ldg(a.pos + t) : 0;
+    const float s_t = on && a.s != nullptr && a.kv.bias != nullptr ? __ldg(a.s + t) : 0.f;
+    // its request: the number of requests that end at or before it (cu_q ascends)
+    int req = 0;
+    int64_t lo = __ldg(a.cu_q), hi = -1, len = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      const bool there = b0 + lane < a.batch;
+      const int end = there ? __ldg(a.cu_q + b0 + lane + 1) : 0x7FFFFFFF;
+      const int l = there ? __ldg(a.kv_len + b0 + lane) : 0;
+#pragma unroll
+      for (int i = 0; i < kAppTok; ++i) {
+        const int n = __popc(__ballot_sync(0xFFFFFFFFu, !there || end > group * tok + i));
+        const int first = 32 - n;  // (the ones before it have ended)
+        const int e = __shfl_sync(0xFFFFFFFFu, end, first & 31);
+        const int before = __shfl_sync(0xFFFFFFFFu, end, (first + 31) & 31);
+        const int el = __shfl_sync(0xFFFFFFFFu, l, first & 31);
+        if (lane == i && hi < 0) {
+          req += first;
+          if (first > 0) lo = before;
+          if (first < 32) {
+            hi = e;
+            len = el;
+          }
+        }
+      }
+    }
+    int64_t page = -1;
+    int row = 0;
+    if (on) {
+      bool bad = req >= a.batch;  // (offsets that do not ascend)
+      if (!bad) {
+        const int64_t dst = len - (hi - lo) + (t - lo);
+        const int64_t blk = dst >> a.kv.page_shift;
+        if (a.pos == nullptr) pos = dst;  // the row's index in its request
+        bad = lo > t || dst < 0 || blk >= a.kv.table_stride;
+        if (!bad) {
+          page = __ldg(a.kv.table + static_cast<int64_t>(req) * a.kv.table_stride + blk);
+          row = static_cast<int>(dst) & (a.kv.page_size - 1);
+          bad = page < 0 || page >= a.kv.n_pages;
+        }
+      }
+      if (bad) {
+        page = -1;
+        report_error(a.err, kErrIndexRange);
+      }
+      if (page >= 0 && a.kv.bias != nullptr)
+        a.kv.bias[page * a.kv.bias_page_stride + row] = a.s ? logsigmoid_f(s_t) : 0.0f;
+    }
+    if (lane < kAppTok) {
+      sm.page[st][lane] = page;
+      sm.pos[st][lane] = pos;
+      sm.row[st][lane] = row;
+    }
+  };
+  auto angles = [&](int st, int meta) {
+    if (!a.rotate) return;
+    for (int e = tid; e < tok * kHalf; e += kAppThreads) {
+      const int i = e / kHalf, f = e % kHalf;
+      const float2 cs = rope_cos_sin_theta(sm.pos[meta][i], a.theta[f]);
+      sm.cos[st][i][app_at<kDh, kVec>(f)] = cs.x;
+      sm.sin[st][i][app_at<kDh, kVec>(f)] = cs.y;
+    }
+  };
+  // this thread's kVec entries of such a table
+  auto entries = [&](const float* table, float2 (&out)[kPairs]) {
+#pragma unroll
+    for (int q = 0; q < kVec / 4; ++q) {
+      const float4 v = *reinterpret_cast<const float4*>(table + q * (kLanes * 4) + sub * 4);
+      out[2 * q] = make_float2(v.x, v.y);
+      out[2 * q + 1] = make_float2(v.z, v.w);
+    }
+  };
+  const bool norm_any = a.q_norm != nullptr || a.k_norm != nullptr;
+  auto work = [&](int64_t group, int st, int meta) {
+    // every lane of a warp reaches the shuffles
+    for (int pass = 0; pass < heads; pass += kHeads) {
+      const int h0 = pass + tid / kLanes;
+      const int kind = h0 < a.hq ? 0 : (h0 < a.hq + a.kv.hkv ? 1 : 2);
+      const int h = kind == 0 ? h0 : (kind == 1 ? h0 - a.hq : h0 - a.hq - a.kv.hkv);
+      const bool norm = kind == 0 ? a.q_norm != nullptr : (kind == 1 && a.k_norm != nullptr);
+      int64_t stride = stride0;
+      const T* src = pass == 0 ? src0 : h0 < heads ? source(h0, stride) : nullptr;
+#pragma unroll 1
+      for (int i = 0; i < tok; ++i) {
+        const int64_t t = group * tok + i;
+        if (t >= total) break;
+        uint4 ulo = make_uint4(0, 0, 0, 0), uhi = ulo;
+        if (pass == 0) {
+          ulo = sm.ring[st][i][0][tid];
+          uhi = sm.ring[st][i][1][tid];
+        } else if (src != nullptr) {
+          ulo = *reinterpret_cast<const uint4*>(src + t * stride);
+          uhi = *reinterpret_cast<const uint4*>(src + t * stride + kHalf);
+        }
+        if (norm_any || a.rotate) {
+          float2 lo[kPairs], hi[kPairs];
+          unpack2(ulo, lo);
+          unpack2(uhi, hi);
+          if (norm_any) {
+            float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) s2 = ffma2(lo[e], lo[e], ffma2(hi[e], hi[e], s2));
+            float ss = s2.x + s2.y;
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+            if (norm) {
+              const float r = rsqrtf(ss * (1.0f / kDh) + a.eps);
+              const float2 r2 = make_float2(r, r);
+              float2 wl[kPairs], wh[kPairs];
+              entries(sm.norm[kind][0], wl);
+              entries(sm.norm[kind][1], wh);
+#pragma unroll
+              for (int e = 0; e < kPairs; ++e) {
+                lo[e] = fmul2(fmul2(lo[e], r2), wl[e]);
+                hi[e] = fmul2(fmul2(hi[e], r2), wh[e]);
+              }
+            }
+          }
+          if (kind < 2) {
+            if (a.rotate) {
+              float2 cs[kPairs], sn[kPairs];
+              entries(sm.cos[st][i], cs);
+              entries(sm.sin[st][i], sn);
+#pragma unroll
+              for (int e = 0; e < kPairs; ++e) {
+                const float2 c = cs[e], s = sn[e], x = lo[e], y = hi[e];
+                lo[e] = ffma2(x, c, fmul2(y, make_float2(-s.x, -s.y)));
+                hi[e] = ffma2(y, c, fmul2(x, s));
+              }
+            }
+            ulo = repack2(lo);
+            uhi = repack2(hi);
+          }
+        }
+        if (h0 >= heads) continue;
+        T* dst;
+        if (kind == 0) {
+          dst = static_cast<T*>(a.q_out) + (t * a.hq + h) * kDh;
+        } else {
+          const int64_t page = sm.page[meta][i];
+          if (page < 0) continue;
+          dst = static_cast<T*>(kind == 1 ? a.kv.k : a.kv.v) +
+                page * (kind == 1 ? a.kv.k_page_stride : a.kv.v_page_stride) +
+                (static_cast<int64_t>(sm.row[meta][i]) * a.kv.hkv + h) * kDh;
+        }
+        *reinterpret_cast<uint4*>(dst + d0) = ulo;
+        *reinterpret_cast<uint4*>(dst + kHalf + d0) = uhi;
       }
     }
   };
-  load(threadIdx.x / kLanes);
-  if (threadIdx.x < nt) {
-    const int i = threadIdx.x;
-    const int64_t t = t0 + i;
-    const int b = i == 0 ? req[0] : i == 1 ? req[1] : i == 2 ? req[2] : req[3];
-    int64_t page = -1;
-    int row = 0;
-    bool bad = false;
-    if (b < a.batch) {  // rows behind the last request are left alone
-      const int64_t lo = __ldg(a.cu_q + b), hi = __ldg(a.cu_q + b + 1);
-      const int64_t dst = static_cast<int64_t>(__ldg(a.kv_len + b)) - (hi - lo) + (t - lo);
-      const int64_t blk = dst >> a.kv.page_shift;
-      bad = lo > t || dst < 0 || blk >= a.kv.table_stride;
-      if (!bad) {
-        page = __ldg(a.kv.table + static_cast<int64_t>(b) * a.kv.table_stride + blk);
-        row = static_cast<int>(dst) & (a.kv.page_size - 1);
-        bad = page < 0 || page >= a.kv.n_pages;
-      }
-    }
-    if (bad) {
-      page = -1;
-      report_error(a.err, kErrIndexRange);
-    }
-    s_dst_page[i] = page;
-    s_dst_row[i] = row;
-    if (page >= 0 && a.kv.bias != nullptr)
-      a.kv.bias[page * a.kv.bias_page_stride + row] = a.s ? logsigmoid_f(__ldg(a.s + t)) : 0.0f;
-  }
-  if (threadIdx.x < kDh) {
-    if (a.q_norm != nullptr) s_norm[0][threadIdx.x] = __ldg(a.q_norm + threadIdx.x);
-    if (a.k_norm != nullptr) s_norm[1][threadIdx.x] = __ldg(a.k_norm + threadIdx.x);
-  }
-  if (a.rotate) {
-    for (int e = threadIdx.x; e < nt * kHalf; e += kAppThreads) {
-      const int i = e / kHalf, f = e % kHalf;
-      int64_t pos;
-      if (a.pos != nullptr) {
-        pos = __ldg(a.pos + t0 + i);
-      } else {  // the row's index in its request
-        const int b = i == 0 ? req[0] : i == 1 ? req[1] : i == 2 ? req[2] : req[3];
-        const int64_t t = t0 + i;
-        pos = b < a.batch ? static_cast<int64_t>(__ldg(a.kv_len + b)) - __ldg(a.cu_q + b + 1) + t : 0;
-      }
-      const float2 cs = rope_cos_sin_theta(pos, a.theta[f]);
-      s_cos[i][f] = cs.x;
-      s_sin[i][f] = cs.y;
+
+  int64_t group = blockIdx.x;
+  if (finder) {
+    find(group, 0);
+  } else {
+    fetch(group, 0);
+    if (tid < kDh) {
+      const int half = tid / kHalf, at = app_at<kDh, kVec>(tid % kHalf);
+      if (a.q_norm != nullptr) sm.norm[0][half][at] = __ldg(a.q_norm + tid);
+      if (a.k_norm != nullptr) sm.norm[1][half][at] = __ldg(a.k_norm + tid);
     }
   }
   __syncthreads();
-  // every lane of a warp reaches the shuffles
-  for (int pass = 0; pass < heads; pass += kHeads) {
-    const int h0 = pass + threadIdx.x / kLanes;
-    if (pass > 0) load(h0);
-    const int kind = h0 < a.hq ? 0 : (h0 < a.hq + a.kv.hkv ? 1 : 2);
-    const int h = kind == 0 ? h0 : (kind == 1 ? h0 - a.hq : h0 - a.hq - a.kv.hkv);
-    const bool norm = kind == 0 ? a.q_norm != nullptr : (kind == 1 && a.k_norm != nullptr);
-    const float* nw = s_norm[kind == 0 ? 0 : 1];
-    const bool work = a.q_norm != nullptr || a.k_norm != nullptr || a.rotate;
-#pragma unroll
-    for (int i = 0; i < kAppTok; ++i) {
-      if (i >= nt) break;
-      const int64_t t = t0 + i;
-      if (work) {
-        float2 lo[kPairs], hi[kPairs];
-        unpack2(ulo[i], lo);
-        unpack2(uhi[i], hi);
-        if (a.q_norm != nullptr || a.k_norm != nullptr) {
-          float2 s2 = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int e = 0; e < kPairs; ++e) s2 = ffma2(lo[e], lo[e], ffma2(hi[e], hi[e], s2));
-          float ss = s2.x + s2.y;
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-          if (norm) {
-            const float r = rsqrtf(ss * (1.0f / kDh) + a.eps);
-            const float2 r2 = make_float2(r, r);
-            const float2* wl = reinterpret_cast<const float2*>(nw + d0);
-            const float2* wh = reinterpret_cast<const float2*>(nw + kHalf + d0);
-#pragma unroll
-            for (int e = 0; e < kPairs; ++e) {
-              lo[e] = fmul2(fmul2(lo[e], r2), wl[e]);
-              hi[e] = fmul2(fmul2(hi[e], r2), wh[e]);
-            }
-          }
-        }
-        if (kind < 2) {
-          if (a.rotate) {
-            const float2* cs = reinterpret_cast<const float2*>(&s_cos[i][d0]);
-            const float2* sn = reinterpret_cast<const float2*>(&s_sin[i][d0]);
-#pragma unroll
-            for (int e = 0; e < kPairs; ++e) {
-              const float2 c = cs[e], s = sn[e], x = lo[e], y = hi[e];
-              lo[e] = ffma2(x, c, fmul2(y, make_float2(-s.x, -s.y)));
-              hi[e] = ffma2(y, c, fmul2(x, s));
-            }
-          }
-          ulo[i] = repack2(lo);
-          uhi[i] = repack2(hi);
-        }
-      }
-      if (req[i] >= a.batch || h0 >= heads) continue;
-      T* dst;
-      if (kind == 0) {
-        dst = static_cast<T*>(a.q_out) + (t * a.hq + h) * kDh;
+  if (!finder) angles(0, 0);
+  else if (group + gridDim.x < groups) find(group + gridDim.x, 1);
+  __syncthreads();
+  for (int st = 0, meta = 0; group < groups; group += gridDim.x, st ^= 1, meta = meta == 2 ? 0 : meta + 1) {
+    const int64_t next = group + gridDim.x;
+    const int meta1 = meta == 2 ? 0 : meta + 1;
+    if (finder) {
+      if (next + gridDim.x < groups) find(next + gridDim.x, meta == 0 ? 2 : meta - 1);
+    } else {
+      if (next < groups) {
+        fetch(next, st ^ 1);
+        angles(st ^ 1, meta1);
       } else {
-        const int64_t page = s_dst_page[i];
-        if (page < 0) continue;
-        dst = static_cast<T*>(kind == 1 ? a.kv.k : a.kv.v) +
-              page * (kind == 1 ? a.kv.k_page_stride : a.kv.v_page_stride) +
-              (static_cast<int64_t>(s_dst_row[i]) * a.kv.hkv + h) * kDh;
+        asm volatile("cp.async.commit_group;" ::: "memory");
       }
-      *reinterpret_cast<uint4*>(dst + d0) = ulo[i];
-      *reinterpret_cast<uint4*>(dst + kHalf + d0) = uhi[i];
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      work(group, st, meta);
     }
+    __syncthreads();
   }
 }
 
@@ -248,7 +339,7 @@ struct SimtSmem {
 };
 
 // 16 bytes global -> shared, zeros where `there` is false
-__device__ __forceinline__ void cp_async16(float* dst, const float* src, bool there) {
+__device__ __forceinline__ void cp_async16_if(float* dst, const float* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
                "r"(there ? 16 : 0)
                : "memory");
@@ -291,8 +382,8 @@ __global__ void __launch_bounds__(kSimtThreads)
       const bool there = page >= 0;
       const float* kp = static_cast<const float*>(a.kv.k);
       const float* vp = static_cast<const float*>(a.kv.v);
-      cp_async16(&sm.k[st][r][c], there ? kp + page * a.kv.k_page_stride + off : kp, there);
-      cp_async16(&sm.v[st][r][c], there ? vp + page * a.kv.v_page_stride + off : vp, there);
+      cp_async16_if(&sm.k[st][r][c], there ? kp + page * a.kv.k_page_stride + off : kp, there);
+      cp_async16_if(&sm.v[st][r][c], there ? vp + page * a.kv.v_page_stride + off : vp, there);
       if (c == 0)
         sm.bias[st][r] =
             there && a.kv.bias ? key_bias(__ldg(a.kv.bias + page * a.kv.bias_page_stride + in)) : 0.f;
@@ -446,11 +537,15 @@ __global__ void __launch_bounds__(kSimtThreads)
 
 template <typename T, int kDh>
 cudaError_t run_append(const PagedAppendArgs& a, cudaStream_t st) {
-  // one token per CTA until every SM has several CTAs
+  // one token a group until every SM has several CTAs
   int tok = 1;
-  while (tok < kAppTok && a.rows / (2 * tok) >= 6 * num_sms()) tok *= 2;
-  const unsigned grid = static_cast<unsigned>((a.rows + tok - 1) / tok);
-  TG_CUDA_TRY(launch_pdl(paged_append<T, kDh>, dim3(grid), dim3(kAppThreads), 0, st, a, tok));
+  while (tok < kAppTok && a.rows / (2 * tok) >= 3 * num_sms()) tok *= 2;
+  const int64_t groups = (a.rows + tok - 1) / tok;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(groups, 3 * num_sms()));
+  auto kern = paged_append<T, kDh>;
+  constexpr int kBytes = static_cast<int>(sizeof(AppSmem<T, kDh>));
+  TG_CUDA_TRY(set_smem_attr_once(reinterpret_cast<const void*>(kern), kBytes));
+  TG_CUDA_TRY(launch_pdl(kern, dim3(grid), dim3(kAppThreads + 32), kBytes, st, a, tok));
   return cudaGetLastError();
 }
 

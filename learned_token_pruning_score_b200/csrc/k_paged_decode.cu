@@ -489,21 +489,46 @@ __global__ void __launch_bounds__(256) paged_merge(const __grid_constant__ Paged
   const int sub = warp % kWarps;  // this warp's share of the splits
   const int idx = static_cast<int>(blockIdx.x) * (8 / kWarps) + warp / kWarps;
   const int t = idx / a.hq, h = idx % a.hq;
-  // rows behind the last request are left alone
-  if (t >= a.rows || t < __ldg(a.cu_q) || t >= __ldg(a.cu_q + a.batch)) return;
+  // Rows behind the last request are left alone. All that is needed is read at
+  // once: the request bounds, the states, and the first rows (of splits without
+  // keys, too: what memory holds there is not used).
+  if (t >= a.rows) return;
+  const int row_lo = __ldg(a.cu_q), row_hi = __ldg(a.cu_q + a.batch);
   constexpr int kN = kDh / 32;
   const int64_t step = a.rows * a.hq;
+  const float* src = a.part_o + static_cast<int64_t>(idx) * kDh + lane * kN;
+  float v[8][kN];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int s = s0 + i * kWarps;
+      const float* p = src + static_cast<int64_t>(s) * step * kDh;
+      if constexpr (kN == 4) {
+        const float4 f = s < a.splits ? __ldcg(reinterpret_cast<const float4*>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[i][0] = f.x;
+        v[i][1] = f.y;
+        v[i][2] = f.z;
+        v[i][3] = f.w;
+      } else {
+        const float2 f = s < a.splits ? __ldcg(reinterpret_cast<const float2*>(p)) : make_float2(0.f, 0.f);
+        v[i][0] = f.x;
+        v[i][1] = f.y;
+      }
+    }
+  };
+  load(sub);
   float m0 = -INFINITY, l0 = 0.f, m1 = -INFINITY, l1 = 0.f;
   if (lane < a.splits) {
-    const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (lane * step + idx) * 2));
-    m0 = v.x;
-    l0 = v.y;
+    const float2 f = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (lane * step + idx) * 2));
+    m0 = f.x;
+    l0 = f.y;
   }
   if (lane + 32 < a.splits) {
-    const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_ml + ((lane + 32) * step + idx) * 2));
-    m1 = v.x;
-    l1 = v.y;
+    const float2 f = __ldcg(reinterpret_cast<const float2*>(a.part_ml + ((lane + 32) * step + idx) * 2));
+    m1 = f.x;
+    l1 = f.y;
   }
+  if (t < row_lo || t >= row_hi) return;
   float top = fmaxf(m0, m1);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
@@ -512,34 +537,15 @@ __global__ void __launch_bounds__(256) paged_merge(const __grid_constant__ Paged
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   float acc[kN] = {};
-  const float* src = a.part_o + static_cast<int64_t>(idx) * kDh + lane * kN;
   const unsigned live0 = __ballot_sync(0xFFFFFFFFu, l0 != 0.f);
   const unsigned live1 = __ballot_sync(0xFFFFFFFFu, l1 != 0.f);
-  // eight rows in flight at a time
   for (int s0 = sub; s0 < a.splits; s0 += 8 * kWarps) {
-    float v[8][kN];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int s = s0 + i * kWarps;
-      const bool live = s < a.splits && (((s < 32 ? live0 : live1) >> (s & 31)) & 1u);
-      const float* p = src + static_cast<int64_t>(s) * step * kDh;
-      if constexpr (kN == 4) {
-        const float4 f = live ? __ldcg(reinterpret_cast<const float4*>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        v[i][0] = f.x;
-        v[i][1] = f.y;
-        v[i][2] = f.z;
-        v[i][3] = f.w;
-      } else {
-        const float2 f = live ? __ldcg(reinterpret_cast<const float2*>(p)) : make_float2(0.f, 0.f);
-        v[i][0] = f.x;
-        v[i][1] = f.y;
-      }
-    }
+    if (s0 != sub) load(s0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int s = s0 + i * kWarps;
       const float w = __shfl_sync(0xFFFFFFFFu, s < 32 ? w0 : w1, s & 31);
-      if (s < a.splits) {
+      if (s < a.splits && (((s < 32 ? live0 : live1) >> (s & 31)) & 1u)) {
 #pragma unroll
         for (int e = 0; e < kN; ++e) acc[e] = fmaf(v[i][e], w, acc[e]);
       }

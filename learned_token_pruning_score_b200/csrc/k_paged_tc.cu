@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_ready = bars + 12;  // and cleaned
   uint64_t* v_empty = bars + 16;
   uint64_t* b_full = bars + 20;   // [4] biases and mask of a tile
-  uint64_t* p_full = bars + 24;   // [A, B][halves of the keys]
+  uint64_t* p_full = bars + 24;   // [A, B]
   uint64_t* s_full = bars + 28;   // [A, B]
   uint64_t* o_full = bars + 30;   // [A, B]
   uint64_t* q_full = bars + 32;
@@ -292,17 +292,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit_warp(&s_full[h]);
         if (h == 1 || both) umma_commit_warp(&k_empty[t % kSt]);
       };
-      auto pv = [&](int h, int t, int half, bool first) {
+      auto pv = [&](int h, int t, bool first) {
         constexpr uint32_t idesc = idesc_bmn(128, kDh);
         const uint64_t vd = sdesc_mn(base + L::kOffV + (t % kSt) * L::kTile, kSub);
         const uint32_t p_tm = tm + static_cast<uint32_t>(h * 128);
         const uint32_t d = tm + 256u + static_cast<uint32_t>(h * 128);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const int ks = half * 4 + kk;
+        for (int ks = 0; ks < kBlk / 16; ++ks)
           umma_f16_ts_warp(d, p_tm + static_cast<uint32_t>(ks * 8), vd + ((ks * 2048) >> 4), idesc,
                            (!first || ks > 0) ? 1u : 0u);
-        }
       };
       auto k_there = [&](int t) -> bool {
         return mbar_wait_warp(&k_full[t % kSt], (t / kSt) & 1, a.err) &&
@@ -328,12 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool more = j + 1 < n;
         const int tk = both ? t + 2 : j + 1;
         if (more && (h == 0 || both) && !k_there(tk)) return false;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!mbar_wait_warp(&p_full[2 * h + half], j & 1, a.err)) return false;
-          tc_fence_after();
-          pv(h, t, half, j == 0);
-        }
+        if (!mbar_wait_warp(&p_full[h], j & 1, a.err)) return false;
+        tc_fence_after();
+        pv(h, t, j == 0);
         if (more) qk(h, tk);
         else umma_commit_warp(&o_full[h]);
         if (h == 1 || both) umma_commit_warp(&v_empty[t % kSt]);
@@ -606,11 +601,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (half == 0) tmem_ld32(s_tm + 64u, y0);
         weights(y1, 2 * half + 1);
         tmem_wait_ld_dep(y0);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[2 * h + half]);  // P V of these keys may start
       }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[h]);
       const float2 s2 = fadd2(fadd2(sp[0], sp[1]), fadd2(sp[2], sp[3]));
       l += s2.x + s2.y;
     }
