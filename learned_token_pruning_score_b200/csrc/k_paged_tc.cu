@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* k_full = bars + 0;
   uint64_t* k_empty = bars + 4;
   uint64_t* v_full = bars + 8;    // the bytes are there
-  uint64_t* v_ready = bars + 12;  // and cleaned
+  uint64_t* go = bars + 12;       // and cleaned; the next tile's keys and biases are there, too
   uint64_t* v_empty = bars + 16;
   uint64_t* b_full = bars + 20;   // [4] biases and mask of a tile
   uint64_t* p_full = bars + 24;   // [A, B]
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 1);
-      mbar_init(&v_ready[i], 1);
+      mbar_init(&go[i], 1);
       mbar_init(&v_empty[i], 1);
       mbar_init(&b_full[i], 1);
       mbar_init(&p_full[i], 4);  // the warps of a warpgroup
@@ -321,15 +321,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int h = decltype(hc)::value;
         const int n = h == 0 ? last_a : last_b;
         const int t = both ? 2 * j + h : j;
-        if ((h == 0 || both) && !mbar_wait_warp(&v_ready[t % kSt], (t / kSt) & 1, a.err)) return false;
-        // the next keys are there by now: P V and the next S go out back to back
+        if ((h == 0 || both) && !mbar_wait_warp(&go[t % kSt], (t / kSt) & 1, a.err)) return false;
         const bool more = j + 1 < n;
-        const int tk = both ? t + 2 : j + 1;
-        if (more && (h == 0 || both) && !k_there(tk)) return false;
         if (!mbar_wait_warp(&p_full[h], j & 1, a.err)) return false;
         tc_fence_after();
         pv(h, t, j == 0);
-        if (more) qk(h, tk);
+        if (more) qk(h, both ? t + 2 : j + 1);
         else umma_commit_warp(&o_full[h]);
         if (h == 1 || both) umma_commit_warp(&v_empty[t % kSt]);
         return true;
@@ -375,10 +372,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_bias(0, bias_pages(0));
         pg = bias_pages(1);
       }
-      // Step i: the biases of tile i, then the values of tile i - 1: the order in
-      // which the MMAs come to need them.
+      // Step i: the biases of tile i, then the values of the tile that it follows in
+      // its warpgroup; with the keys of tile i that is all that P V of the one
+      // and Q K of the other need, and the MMAs wait for it once.
+      const int dt = dual ? 2 : 1;
 #pragma unroll 1
-      for (int i = 0; i <= nt; ++i) {
+      for (int i = 0; i < nt + dt; ++i) {
         if (kBias && i < nt) {
           // QK(i - 2) has read its K-step; so the softmax of tile i - 4 is over
           if (i >= 2 && !mbar_wait_warp(&k_empty[(i - 2) % kSt], ((i - 2) / kSt) & 1, a.err)) break;
@@ -400,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_bias(i + 1, pg);
           pg = bias_pages(i + 2);
         }
-        const int t = i - 1;
+        const int t = i - dt;
         if (t < 0) continue;
         const int s = t % kSt, key0 = lo + t * kBlk;
         uint4 part = make_uint4(0u, 0u, 0u, 0u);  // keys that their bias may remove
@@ -428,7 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_async_smem();
           __syncwarp();
         }
-        if (lane == 0) mbar_arrive(&v_ready[s]);
+        if (i < nt && !mbar_wait_warp(&k_full[i % kSt], (i / kSt) & 1, a.err)) break;
+        if (lane == 0) mbar_arrive(&go[s]);
       }
     }
   } else {
@@ -517,90 +517,99 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st32_wait(s_tm + static_cast<uint32_t>(c * 32), z);
         }
       }
-      // The row's maximum, 64 logits at a time.
-      float mx = -INFINITY;
-#pragma unroll 1
-      for (int c = 0; c < 128; c += 64) {
-        uint32_t u0[32], u1[32];
-        tmem_ld32(s_tm + static_cast<uint32_t>(c), u0);
-        tmem_ld32(s_tm + static_cast<uint32_t>(c + 32), u1);
-        tmem_wait_ld_dep(u1);
-        tmem_ld_fence(u0);
+      // P = 2^(S scale2 - m), 32 keys at a time, in packed pairs, one pair in four
+      // on the FMA pipe (the MUFU unit is this loop's bottleneck); 32 keys' P covers
+      // 16 columns of logits that have been read. The running maximum m is moved
+      // (to a whole number, so that every rescaling is by an exact power of two)
+      // only when 32 logits pass it by more than 2^8, after their exponentials: no
+      // pass over the row comes before them (2048 tokens after 30720, no bias: 482
+      // us with one, 470 without). What the row has gathered, the P of this tile
+      // included, is rescaled then, and the 32 exponentials are formed again.
+      float2 sp[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                      make_float2(0.f, 0.f)};
+      const float2 sc2 = make_float2(scale2, scale2);
+      float base = m == -INFINITY ? 0.f : m;
+      uint32_t y0[32];
+      auto weights = [&](uint32_t (&u)[32], int c) {
         float mx4[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mx4[k] = fmax3f(__uint_as_float(u0[k]), __uint_as_float(u0[4 + k]), __uint_as_float(u1[k]));
+          mx4[k] = fmax3f(__uint_as_float(u[k]), __uint_as_float(u[4 + k]), __uint_as_float(u[8 + k]));
 #pragma unroll
-        for (int i = 8; i < 32; i += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mx4[k] = fmax3f(mx4[k], __uint_as_float(u0[i + k]), __uint_as_float(u0[i + 4 + k]));
-#pragma unroll
-        for (int i = 4; i < 28; i += 8)
+        for (int i = 12; i < 28; i += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mx4[k] = fmax3f(mx4[k], __uint_as_float(u1[i + k]), __uint_as_float(u1[i + 4 + k]));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mx4[k] = fmaxf(mx4[k], __uint_as_float(u1[28 + k]));
-        mx = fmax3f(mx, fmax3f(mx4[0], mx4[1], mx4[2]), mx4[3]);
-      }
-      mx *= scale2;
-      float alpha = 1.0f;
-      if (mx > m + kRescale || (m == -INFINITY && mx != -INFINITY)) {
-        alpha = ex2_approx(m - mx);  // 0 on the first keys
-        l *= alpha;
-        m = mx;
-      }
-      if (j > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
-#pragma unroll 1
-        for (int c = 0; c < kDh / 32; ++c) {
-          float o[32];
-          const uint32_t ta = o_tm + static_cast<uint32_t>(c * 32);
-          tmem_ld32_wait(ta, o);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= alpha;
-          tmem_st32_wait(ta, o);
-        }
-      }
-      // P = 2^(S scale2 - m), 32 keys at a time (read again from TMEM: held in
-      // registers from the maximum on, the 128 logits unroll this loop to a
-      // size that the instruction cache does not hold beside the other warps'
-      // code), in packed pairs, one pair in four on the FMA pipe (the MUFU unit
-      // is this loop's bottleneck). 32 keys' P covers 16 columns of logits that
-      // have been read.
-      const float base = m == -INFINITY ? 0.f : m;
-      float2 sp[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                      make_float2(0.f, 0.f)};
-      const float2 sc2 = make_float2(scale2, scale2), nm2 = make_float2(-base, -base);
-      uint32_t y0[32], y1[32];
-      auto weights = [&](uint32_t (&u)[32], int c) {
+            mx4[k] = fmax3f(mx4[k], __uint_as_float(u[i + k]), __uint_as_float(u[i + 4 + k]));
+        const float mx = fmaxf(fmax3f(mx4[0], mx4[1], mx4[2]),
+                               fmax3f(mx4[3], fmax3f(__uint_as_float(u[28]), __uint_as_float(u[29]),
+                                                     __uint_as_float(u[30])),
+                                      __uint_as_float(u[31]))) *
+                         scale2;
         uint32_t pk[16];
+        float2 cs[4];
+        // with the maximum as it stands; once more when these logits move it
+#pragma unroll 1
+        for (bool again = false;; again = true) {
+          const float2 nm2 = make_float2(-base, -base);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 y =
-              ffma2(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), sc2, nm2);
-          float2 e;
-          if ((i & 3) == 3) {
-            e = exp2_fma(y);
-          } else {
-            e.x = ex2_approx(y.x);
-            e.y = ex2_approx(y.y);
+          for (int i = 0; i < 16; ++i) {
+            const float2 y =
+                ffma2(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), sc2, nm2);
+            float2 e;
+            if ((i & 3) == 3) {
+              e = exp2_fma(y);
+            } else {
+              e.x = ex2_approx(y.x);
+              e.y = ex2_approx(y.y);
+            }
+            cs[i & 3] = i < 4 ? e : fadd2(cs[i & 3], e);
+            pk[i] = pack_bf16x2(e.x, e.y);
           }
-          sp[i & 3] = fadd2(sp[i & 3], e);
-          pk[i] = pack_bf16x2(e.x, e.y);
+          if (again) break;
+          const bool grow = mx > m + kRescale || (m == -INFINITY && mx != -INFINITY);
+          if (!__any_sync(0xFFFFFFFFu, grow)) break;
+          float alpha = 1.0f;
+          if (grow) {
+            const float m_new = ceilf(mx);
+            alpha = ex2_approx(m - m_new);  // 0 on the first keys
+            m = base = m_new;
+          }
+          l *= alpha;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sp[k] = fmul2(sp[k], make_float2(alpha, alpha));
+          tmem_wait_st();
+#pragma unroll 1
+          for (int e = 0; e < c; ++e) {
+            uint32_t old[16];
+            tmem_ld16(s_tm + static_cast<uint32_t>(16 * e), old);
+            tmem_wait_ld_dep16(old);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              old[i] = pack_bf16x2(__uint_as_float(old[i] << 16) * alpha,
+                                   __uint_as_float(old[i] & 0xFFFF0000u) * alpha);
+            tmem_st16(s_tm + static_cast<uint32_t>(16 * e), old);
+          }
+          if (j > 0) {
+#pragma unroll 1
+            for (int e = 0; e < kDh / 32; ++e) {
+              float o[32];
+              const uint32_t ta = o_tm + static_cast<uint32_t>(e * 32);
+              tmem_ld32_wait(ta, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= alpha;
+              tmem_st32_wait(ta, o);
+            }
+          }
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sp[k] = fadd2(sp[k], cs[k]);
         tmem_st16(s_tm + static_cast<uint32_t>(16 * c), pk);
       };
-      tmem_ld32(s_tm, y0);
-      tmem_wait_ld_dep(y0);
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        tmem_ld32(s_tm + static_cast<uint32_t>(64 * half + 32), y1);
-        weights(y0, 2 * half);
-        tmem_wait_ld_dep(y1);
-        if (half == 0) tmem_ld32(s_tm + 64u, y0);
-        weights(y1, 2 * half + 1);
+      for (int c = 0; c < 4; ++c) {
+        tmem_ld32(s_tm + static_cast<uint32_t>(32 * c), y0);
         tmem_wait_ld_dep(y0);
+        weights(y0, c);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -615,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ok = ok && (n_h[h] == 0 || mbar_wait_warp(&o_full[h], 0, a.err));
     if (dual && h == 1) ok = ok && mbar_wait_warp(&o_full[0], 0, a.err);  // all MMAs have read K
     // the last tile's values are cleaned: s_found is final
-    ok = ok && mbar_wait_warp(&v_ready[(nt - 1) % kSt], ((nt - 1) / kSt) & 1, a.err);
+    ok = ok && mbar_wait_warp(&go[(nt - 1) % kSt], ((nt - 1) / kSt) & 1, a.err);
     tc_fence_after();
     float4* xo = reinterpret_cast<float4*>(smem + L::kOffK) + r;  // [kDh / 4][128 rows]
     float wa = 1.0f, wb = 0.f;
