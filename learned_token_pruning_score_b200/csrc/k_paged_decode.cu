@@ -20,6 +20,7 @@
 // softmax would run one thread per row; here all 128 threads hold logits, and
 // the tensor work is a few percent of the time that the keys take to arrive.
 #include <algorithm>
+#include <atomic>
 
 #include "tg_device.cuh"
 #include "tg_internal.h"
@@ -596,9 +597,17 @@ cudaError_t run(const PagedAttnArgs& a, int64_t tiles, bool cluster, cudaStream_
   const int64_t grid = tiles * a.splits * a.kv.hkv;
   auto launch = [&](auto kern, int cluster) -> cudaError_t {
     TG_CUDA_TRY(set_smem_attr_once(reinterpret_cast<const void*>(kern), static_cast<int>(C::kSmem)));
-    if (cluster > 8)
-      TG_CUDA_TRY(cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+    if (cluster > 8) {  // once for each device
+      static std::atomic<uint64_t> allowed{0};
+      int dev = 0;
+      TG_CUDA_TRY(cudaGetDevice(&dev));
+      const uint64_t bit = uint64_t(1) << (dev & 63);
+      if (!(allowed.load() & bit)) {
+        TG_CUDA_TRY(cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                         cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+        allowed.fetch_or(bit);
+      }
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kThreads);
