@@ -87,15 +87,13 @@ struct QuantRow {
 // Four integers in a word.
 __device__ __forceinline__ uint32_t quantize4(const float (&f)[4], const QuantRow& a) {
   constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
-  uint32_t q[4];
-  float e[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float t = fmaf(f[i], a.r, kMagic);
-    q[i] = __float_as_uint(t);
-    e[i] = fabsf(fmaf(f[i], a.r, kMagic - t));
-  }
-  const float worst = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
+  const float2 magic = make_float2(kMagic, kMagic), r = make_float2(a.r, a.r), one = make_float2(-1.f, -1.f);
+  const float2 x = make_float2(f[0], f[1]), y = make_float2(f[2], f[3]);
+  const float2 tx = ffma2(x, r, magic), ty = ffma2(y, r, magic);
+  const float2 ex = ffma2(x, r, ffma2(tx, one, magic)), ey = ffma2(y, r, ffma2(ty, one, magic));
+  uint32_t q[4] = {__float_as_uint(tx.x), __float_as_uint(tx.y), __float_as_uint(ty.x),
+                   __float_as_uint(ty.y)};
+  const float worst = fmaxf(fmax3f(fabsf(ex.x), fabsf(ex.y), fabsf(ey.x)), fabsf(ey.y));
   if (!(worst <= 0.49999f)) {  // (127 / amax infinite: NaN, or 1e7 and more)
 #pragma unroll
     for (int i = 0; i < 4; ++i) q[i] = quantize_exact(f[i] * a.shift, a.r_near, a.amax);
