@@ -18,7 +18,7 @@
 //
 // Why mma.sync: 16 rows use an eighth of a tcgen05 tile (M = 128), whose
 // softmax would run one thread per row; here all 128 threads hold logits, and
-// the tensor work is a few percent of the time that the keys take to arrive.
+// the tensor work is a fifth of the time that the keys take to arrive.
 #include <algorithm>
 #include <atomic>
 
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   pdl_wait();
   if (warp == 0) {
-    const PagedTile t = find_tile(a, kRows, tile_idx);
+    const PagedTile t = find_tile<kRows>(a, tile_idx);
     if (lane == 0) s_tile = t;
   }
   __syncthreads();
@@ -634,7 +634,7 @@ cudaError_t launch_paged_merge(const PagedAttnArgs& a, bool bf16, cudaStream_t s
 }
 
 cudaError_t launch_paged_decode(PagedAttnArgs a, void* ws, cudaStream_t st) {
-  const int64_t tiles = paged_row_tiles(a.rows, a.batch, a.hq, a.kv.hkv, kRows);
+  const int64_t tiles = a.tiles = paged_row_tiles(a.rows, a.batch, a.hq, a.kv.hkv, kRows);
   const int64_t jobs = tiles * a.kv.hkv;
   // Few jobs over keys that 16 splits of 128 hold: a cluster for each, which
   // merges its splits itself (one token, 8 KV heads: 1000 keys 8.8 us, 2000

@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   if (warp == 0) {
-    const PagedTile t = find_tile(a, 2 * kBlk, tile_idx);
+    const PagedTile t = find_tile<2 * kBlk>(a, tile_idx);
     if (lane == 0) s_tile = t;
   }
   __syncthreads();

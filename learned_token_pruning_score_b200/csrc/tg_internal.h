@@ -392,11 +392,17 @@ struct PagedAttnArgs {
   float* part_o;                    // [splits][rows][hq][dh], unnormalised
   float* part_ml;                   // [splits][rows][hq][2]: maximum (log2 units) and sum
 };
-// Upper bound of the row tiles of a call: rows are (token, head of the group)
-// pairs and each request's last tile may be short.
+// Row tiles are dealt to slots; rows are (token, head of the group) pairs and each
+// request's last tile may be short. The first slot of request b, which begins
+// at token cu, is a bound of the tiles before it, so that it needs no count of
+// them: x rows fill at most (x - 1) / tile + 1 tiles, and a token no more than
+// ceil(group / tile), the closer bound where most requests are empty.
+__host__ __device__ inline int64_t paged_first_slot(int64_t cu, int64_t b, bool sparse, int group,
+                                                    int tile) {
+  return sparse ? cu * ((group + tile - 1) / tile) : (cu * group + b * (tile - 1)) / tile;
+}
 inline int64_t paged_row_tiles(int64_t rows, int64_t batch, int hq, int hkv, int tile) {
-  const int64_t requests = batch < rows ? batch : rows;
-  return (rows * (hq / hkv) - requests) / tile + requests;
+  return paged_first_slot(rows, batch, rows < batch, hq / hkv, tile);
 }
 // bf16: rows of a tile. Up to 16 rows of a request and KV head on average the
 // keys are what the call is made of (16, k_paged_decode.cu); above, the tensor

@@ -218,6 +218,42 @@ def test_unaligned_scales_are_refused_or_read():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("most,dtype", [(1, BF), (6, BF), (40, BF), (1, F32), (40, F32)])
+def test_thousands_of_requests(most, dtype):
+    """Requests found among thousands, empty ones between them, by the append
+    and by each of the attention's row tiles."""
+    r = torch.Generator().manual_seed(most)
+    n = torch.randint(0, most + 1, (2500,), generator=r)
+    p = torch.randint(0, 40, (2500,), generator=r)
+    n[100:170], n[-1] = 0, most
+    st = Setup(list(zip(n.tolist(), p.tolist())), 4, 2, 64, 16, dtype, seed=53, stale=5.0)
+    x = torch.randn(st.rows, 8, 64, generator=st.g, device="cuda").to(dtype)
+    st.fill()
+    before = st.k.clone()
+    q = tg.tg_paged_append(st.cache, x[:, 4:6], x[:, 6:], st.cu, st.kv_len, q=x[:, :4], rope_base=0.0)
+    owner = torch.repeat_interleave(torch.arange(2500), n).cuda()
+    row = torch.arange(st.rows, device="cuda") - st.cu[owner].long() + p.cuda()[owner]
+    pg, at = st.table[owner, row // 16].long(), row % 16
+    assert torch.equal(st.k[pg, at], x[:, 4:6]) and torch.equal(st.v[pg, at], x[:, 6:])
+    untouched = torch.ones(st.k.shape[:2], dtype=torch.bool, device="cuda")
+    untouched[pg, at] = False
+    assert torch.equal(st.k[untouched], before[untouched])
+    out = tg.tg_paged_attn(st.cache, q, st.cu, st.kv_len)
+    # the same requests a few at a time
+    for b0 in (0, 90, 1203, 2490):
+        sub = tg.PagedKV(st.k, st.v, st.table[b0:b0 + 10].contiguous(), st.bias)
+        lo, hi = st.cu_host[b0], st.cu_host[b0 + 10]
+        cu = (st.cu[b0:b0 + 11] - lo).contiguous()
+        part = tg.tg_paged_attn(sub, q[lo:hi], cu, st.kv_len[b0:b0 + 10].contiguous())
+        # The weights and the output are rounded once in either call, each by at
+        # most 2^-8 of the largest value; in fp32 the logits' sums of 64 products are
+        # what differs, and each moves a weight and the sum that divides it.
+        logit = 64 * float(q.abs().max()) * float(st.k.abs().max()) / 8
+        unit = 2.0 ** -8 if dtype == BF else 64 * 2.0 ** -24 * logit
+        tol = 4 * unit * float(st.v.abs().max())
+        assert ((part.float() - out[lo:hi].float()).abs() <= tol).all()
+
+
 def test_append_many_requests_and_heads():
     """More requests than a warp counts at once, more heads than a pass holds,
     more tokens than the blocks' first groups."""
