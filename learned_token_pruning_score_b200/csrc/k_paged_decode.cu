@@ -650,12 +650,16 @@ cudaError_t launch_paged_decode(PagedAttnArgs a, void* ws, cudaStream_t st) {
     a.chunk0 = a.chunk;
     return a.kv.dh == 128 ? run<128>(a, tiles, cluster > 1, st) : run<64>(a, tiles, cluster > 1, st);
   }
-  // Enough splits for every SM's two CTAs (a wave more when requests may
-  // differ in length), of 128 keys at least; long ones in pieces of 4096 keys,
+  // Splits for every SM's two CTAs, of 128 keys at least. Few jobs, whose pieces
+  // are short: one wave of them (2 requests of 1000 to 9000 keys, 16 jobs: 16
+  // splits 23 us, 37 27; 4 requests of 2000, 32 jobs: 9 splits 18, 18 22). More:
+  // two, since the pieces of short requests leave their SMs idle (30 requests of
+  // 1000 to 9000 keys, 60 jobs: 9 splits 51, 4 65). Long ones in pieces of 4096 keys,
   // so that the last CTAs to finish have little left (64 requests of 500 to 32768
   // keys: pieces of 1024 keys 754 us, 2048 666, 4096 643, 8192 649).
   const int most = paged_max_splits(a.rows, a.hq, a.kv.dh);
-  const int64_t want = std::max<int64_t>(1, (a.batch == 1 ? 2 : 4) * num_sms() / jobs);
+  const int64_t waves = a.batch == 1 || 8 * jobs <= 2 * num_sms() ? 1 : 2;
+  const int64_t want = std::max<int64_t>(1, waves * 2 * num_sms() / jobs);
   int64_t chunk = std::max<int64_t>(128, (a.max_kv + want - 1) / want);
   if (chunk > 4096) chunk = 4096;
   chunk = std::max<int64_t>(chunk, (a.max_kv + most - 1) / most);
