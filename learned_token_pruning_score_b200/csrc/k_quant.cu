@@ -254,12 +254,15 @@ cudaError_t launch_quantize_rows(const void* x, int64_t x_stride, int64_t rows, 
 cudaError_t launch_quant_gemm(const QuantGemmArgs& g, cudaStream_t st) {
   if (g.m <= 0) return cudaSuccess;
   // Up to four rows the warps' dot products need no tensor core (1 x 4096 x
-  // 2048: 3.9 us, narrow 4.9). Above, the narrow tiles until the wide ones
-  // come near to a wave of CTA pairs (200 x 4096 x 2048, 16 wide tiles: narrow
-  // 10.2 us, wide 14.2; 1024 x 4096 x 2048, 64: 14.7 and 14.6; 512 x 12288 x
-  // 2048, 96: 26.1 and 21.3).
+  // 2048: 3.9 us, narrow 4.9). Above, the narrow tiles, whose k can be split,
+  // until the wide ones fill a third of the SMs (512 x 2048, 16 wide tiles: k =
+  // 1024 narrow 9.9 us, wide 9.5; 6144 18.8 and 21.6; 700 x 2048, 24: 10.2 and 9.5,
+  // 22.6 and 23.8; 1024 x 2048, 32: 10.7 and 9.6, 24.7 and 22.7); to a wave of them
+  // where a wide tile would be half empty (64 x 12288 x 2048, 48: 10.2 and 13.9).
   const int64_t wide_tiles = (g.m + 255) / 256 * ((g.n + 255) / 256);
-  if (g.m > 4) return wide_tiles < 64 ? launch_quant_gemm_narrow(g, st) : launch_quant_gemm_wide(g, st);
+  if (g.m > 4)
+    return wide_tiles < (g.m <= 128 ? 64 : 24) ? launch_quant_gemm_narrow(g, st)
+                                               : launch_quant_gemm_wide(g, st);
   const dim3 grid(static_cast<unsigned>((g.n + 8 * kGvCols - 1) / (8 * kGvCols)),
                   static_cast<unsigned>((g.m + kGvRows - 1) / kGvRows));
   if (g.bf16) TG_CUDA_TRY(launch_pdl(quant_gemv<__nv_bfloat16>, grid, dim3(256), 0, st, g));

@@ -86,6 +86,20 @@ struct Wide {
   static constexpr size_t kSmem = 1024 + kOffBar + 256;
 };
 
+// The residual of a piece of 32 rows x 128 bytes, 4 rows an instruction.
+template <typename T>
+__device__ __forceinline__ void load_residual(const Params& p, int64_t row0, int col, uint4 (&t)[8]) {
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const int64_t c0 = col + (lane & 7) * (16 / static_cast<int>(sizeof(T)));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t r = row0 + 4 * i + (lane >> 3);
+    t[i] = make_uint4(0, 0, 0, 0);
+    if (r < p.m && c0 < p.n)
+      t[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.residual) + r * p.n + c0);
+  }
+}
+
 // One warp's 32 rows x 128 bytes of outputs (64 bf16 or 32 fp32 columns from
 // column `col` on): the accumulators, scaled, plus the residual, into `buf`
 // (rows of 128 bytes, 16-byte unit u of row r at u ^ (r & 7), the layout of
@@ -93,32 +107,29 @@ struct Wide {
 // piece of 128 bytes far from its neighbour's: stored and read directly it
 // costs a sector per thread and instruction, which made the epilogue the
 // longer side of a tile at k = 2048 (8192 x 12288: 180 us).
+// `ahead` holds the piece's residual and receives the one of the next piece
+// (columns from next_col of the rows from next_row), which is on its way
+// while this one is scaled (8192 x 2048 x 272 onto a residual: read where it
+// is added 44 us, a piece ahead 41, asked into L2 a tile ahead as well 37; two
+// pieces ahead 36, with twice the code).
 template <typename T>
 __device__ __forceinline__ void scale_store(const Params& p, const CUtensorMap* tmY, int64_t row0,
-                                            int col, float xs, uint32_t t_col, uint8_t* buf) {
+                                            int col, float xs, uint32_t t_col, uint8_t* buf,
+                                            uint4 (&ahead)[8], int64_t next_row, int next_col) {
   constexpr int kVec = 16 / static_cast<int>(sizeof(T));  // outputs of a 16-byte unit
   constexpr int kCols = 8 * kVec;
   const int lane = static_cast<int>(threadIdx.x & 31);
-  // the residual, 4 rows of 128 bytes an instruction
   const bool res = p.residual != nullptr;
-  const int u = lane & 7;
-  const int64_t c0 = col + u * kVec;
   if (res) {
-    uint4 t[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t r = row0 + 4 * i + (lane >> 3);
-      t[i] = make_uint4(0, 0, 0, 0);
-      if (r < p.m && c0 < p.n)
-        t[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.residual) + r * p.n + c0);
-    }
     if (lane == 0) bulk_wait_read_but_one();  // the store that last used buf has read it
     __syncwarp();
+    const int u = lane & 7;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = 4 * i + (lane >> 3);
-      *reinterpret_cast<uint4*>(buf + r * 128 + ((u ^ (r & 7)) << 4)) = t[i];
+      *reinterpret_cast<uint4*>(buf + r * 128 + ((u ^ (r & 7)) << 4)) = ahead[i];
     }
+    load_residual<T>(p, next_row, next_col, ahead);
   } else if (lane == 0) {
     bulk_wait_read_but_one();
   }
@@ -278,21 +289,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {
     const int quarter = warp & 3;
     uint8_t* out = tiles + C::kOffOut + quarter * 8192;
+    constexpr int kStep = 128 / static_cast<int>(sizeof(T));
     int flip = 0;
     int it = 0;
+    auto first_row = [&](int tile) {
+      return static_cast<int64_t>(tile / p.tiles_n) * 256 + rank * 128 + quarter * 32;
+    };
+    // A piece ahead leaves too few bytes on their way from DRAM: the next tile's
+    // residual is asked into L2 a tile ahead, each lane's row of it.
+    auto prefetch = [&](int tile) {
+      const int64_t r = first_row(tile) + lane;
+      const int col = tile % p.tiles_n * 256;
+      if (r >= p.m) return;
+      const T* at = static_cast<const T*>(p.residual) + r * p.n + col;
+#pragma unroll
+      for (int c = 0; c < 256; c += kStep)
+        if (col + c < p.n) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + c));
+    };
+    if (p.residual != nullptr) prefetch(pair);
+    uint4 ahead[8];
+    if (p.residual != nullptr) load_residual<T>(p, first_row(pair), pair % p.tiles_n * 256, ahead);
     for (int tile = pair; tile < num_tiles; tile += n_pairs, ++it) {
-      const int mb = tile / p.tiles_n, nb = tile % p.tiles_n;
+      const int nb = tile % p.tiles_n;
       const int a = it & 1;
       if (!mbar_wait_warp(&acc_full[a], static_cast<uint32_t>(it >> 1) & 1u, p.err)) break;
       tc_fence_after();
-      const int64_t row0 = static_cast<int64_t>(mb) * 256 + rank * 128 + quarter * 32;
+      const int64_t row0 = first_row(tile);
+      // (behind the last tile: rows past m, of which nothing is read)
+      const int64_t next_row = tile + n_pairs < num_tiles ? first_row(tile + n_pairs) : p.m;
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                              static_cast<uint32_t>(a * 256);
       const float xs = row0 + lane < p.m ? __ldg(p.xs + row0 + lane) : 0.f;
-      constexpr int kStep = 128 / static_cast<int>(sizeof(T));
+      if (p.residual != nullptr && tile + n_pairs < num_tiles) prefetch(tile + n_pairs);
 #pragma unroll 1
       for (int c = 0; c < 256; c += kStep) {
-        scale_store<T>(p, &tmY, row0, nb * 256 + c, xs, t_row + c, out + (flip ? 4096 : 0));
+        const bool last = c + kStep == 256;
+        scale_store<T>(p, &tmY, row0, nb * 256 + c, xs, t_row + c, out + (flip ? 4096 : 0), ahead,
+                       last ? next_row : row0,
+                       last ? (tile + n_pairs) % p.tiles_n * 256 : nb * 256 + c + kStep);
         flip ^= 1;
       }
       tc_fence_before();
@@ -560,12 +594,19 @@ cudaError_t run_narrow(const QuantGemmArgs& g, cudaStream_t st) {
     return cudaErrorInvalidValue;
   const int tiles_n = (g.n + 127) / 128;
   const int tiles_m = static_cast<int>((g.m + C::kMaxCols - 1) / C::kMaxCols);
-  // k is split until the next doubling would pass one CTA an SM, each CTA keeping
-  // two stages of k at least (64 x 4096 x 2048: 4 parts, 128 CTAs, 7.2 us, 8 parts
-  // 7.9; 128 x 12288 x 2048: 1 part, 96 CTAs, 14.5 us, 2 parts 15.6).
+  // k is split while one CTA an SM holds the parts. Into four as soon as there
+  // are four blocks of k (64 x 2048 x 608: 1 part 6.1 us, 2 parts 7.3, 4 parts
+  // 5.8; 128 x 2048 x 4096: 16.4, 14.6, 9.3); into eight where SMs stay idle or
+  // the parts are long (64 x 1024 x 1024: 4 parts 5.7, 8 parts 5.2; 128 x 2048 x
+  // 2048, 128 CTAs: 8.2 and 8.9; 64 x 2048 x 6144: 8.5 and 7.9). Two parts add up
+  // half a tile each, which only a long k repays (512 x 2048: k = 2048 12.3 us,
+  // 2 parts 13.6; 6144 21.6 and 18.8).
   const int num_kb = (g.k + kBK - 1) / kBK;
+  const int tiles = tiles_n * tiles_m;
   int split = 1;
-  while (split < 8 && tiles_n * tiles_m * split * 2 <= num_sms() && num_kb >= 4 * split) split *= 2;
+  if (tiles * 8 <= num_sms() && num_kb >= (tiles * 16 <= num_sms() ? 8 : 32)) split = 8;
+  else if (tiles * 4 <= num_sms() && num_kb >= 4) split = 4;
+  else if (tiles * 2 <= num_sms() && num_kb >= 28) split = 2;
   p.stages = C::kRing / (C::kWBytes + p.cols * kBK);
   if (p.stages > C::kMaxStages) p.stages = C::kMaxStages;
   auto kern = gemm_i8_narrow<T>;

@@ -183,6 +183,23 @@ def test_linear_tails(m, n, k, dtype, residual):
     check_linear(m, n, k, dtype, residual, seed=m + n, lo=-128)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("m,n,k", [(100, 160, 512), (300, 1024, 400), (70, 256, 1040), (520, 2048, 3600),
+                                   (700, 2048, 64), (6622, 928, 48), (4096, 96, 640)])
+def test_linear_plans(m, n, k, dtype):
+    """Each number of parts of k, wide tiles below and above a wave, with the
+    residual that the product overwrites."""
+    check_linear(m, n, k, dtype, True, seed=m, lo=-128)
+    g = gen(m)
+    xq, xs = tg.tg_quantize_rows(torch.randn(m, k, generator=g, device="cuda"))
+    wq, ws = tg.tg_quantize_rows(torch.randn(n, k, generator=g, device="cuda"))
+    r = torch.randn(m, n, generator=g, device="cuda").to(dtype)
+    want = tg.tg_linear_quantized(xq, xs, wq, ws, residual=r, dtype=dtype)
+    y = r.clone()
+    tg.tg_linear_quantized(xq, xs, wq, ws, residual=y, y=y, dtype=dtype)
+    assert torch.equal(y, want)
+
+
 def test_linear_on_the_first_rows_of_a_buffer():
     """y is a part of a larger buffer: nothing behind it is written."""
     g = gen(46)
