@@ -46,6 +46,9 @@ constexpr int kBlk = 128;          // rows of a warpgroup = keys of a tile
 constexpr int kThreads = 384;
 constexpr int kSub = 128 * 128;    // [128 rows x 64 bf16], 128-byte swizzle
 constexpr float kRescale = 8.0f;   // log2 units
+// From this maximum on (log2 units) a logit is rounded before the maximum is
+// taken off it: see the loop of the exponentials.
+constexpr float kFarMax = 4194304.0f;  // 2^22
 
 template <int kDh>
 struct Lay {
@@ -510,6 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_arrive(q_full);
     float m = -INFINITY, l = 0.f;
+    bool far = false;  // some row of the warp has its maximum at 2^22 or beyond
     bool ok = true;
     for (int j = 0; j < n_h[h] && ok; ++j) {
       const int t = dual ? 2 * j + h : j;
@@ -559,10 +563,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       // included, is rescaled then, and the 32 exponentials are formed again.
       float2 sp[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                       make_float2(0.f, 0.f)};
-      const float2 sc2 = make_float2(scale2, scale2);
+      // The product S scale2 is exact in the FMA, but the maximum comes from the rounded
+      // product, half a unit in its last place away: from 2^22 on that is a quarter and
+      // more (512 where a gate bias of -1e10 holds every key: the largest weight would be
+      // 2^512 or 0). There (`far`) the logits are rounded like their maximum, before the
+      // loop, whose factor is then 1. (2048 tokens after 30720: 515 us with this, 511
+      // without; 541 with the far logits' exponentials formed anew behind the loop, 594
+      // with the rounding inside it.)
       float base = m == -INFINITY ? 0.f : m;
       uint32_t y0[32];
-      auto weights = [&](uint32_t (&u)[32], int c) {
+      auto round_logits = [&](uint32_t (&u)[32]) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * scale2);
+      };
+      auto weights = [&](uint32_t (&u)[32], int c, float factor) {
         float mx4[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -576,13 +590,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                fmax3f(mx4[3], fmax3f(__uint_as_float(u[28]), __uint_as_float(u[29]),
                                                      __uint_as_float(u[30])),
                                       __uint_as_float(u[31]))) *
-                         scale2;
+                         factor;
         uint32_t pk[16];
         float2 cs[4];
         // with the maximum as it stands; once more when these logits move it
 #pragma unroll 1
         for (bool again = false;; again = true) {
-          const float2 nm2 = make_float2(-base, -base);
+          const float2 nm2 = make_float2(-base, -base), sc2 = make_float2(factor, factor);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float2 y =
@@ -605,6 +619,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float m_new = ceilf(mx);
             alpha = ex2_approx(m - m_new);  // 0 on the first keys
             m = base = m_new;
+          }
+          far = __any_sync(0xFFFFFFFFu, fabsf(base) >= kFarMax);
+          if (far && factor != 1.0f) {
+            round_logits(u);
+            factor = 1.0f;
           }
           l *= alpha;
 #pragma unroll
@@ -641,7 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < 4; ++c) {
         tmem_ld32(s_tm + static_cast<uint32_t>(32 * c), y0);
         tmem_wait_ld_dep(y0);
-        weights(y0, c);
+        if (far) round_logits(y0);
+        weights(y0, c, far ? 1.0f : scale2);
       }
       tmem_wait_st();
       tc_fence_before();
