@@ -94,11 +94,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // 1.5 * 2^23 leaves it in the low mantissa bits), a degree-3 polynomial for
 // 2^f, |f| <= 1/2, fitted here with p(0) = 1 (largest relative error 1.02e-4),
 // and j added to the exponent field. Below -127 that gives exactly 0, so a
-// masked logit (-inf) has no weight; a NaN comes out as 3e38 (infinity in
-// bf16) and so still shows in the output.
+// masked logit (-inf) has no weight. So does a NaN: its row is marked where the
+// maximum is formed.
 __device__ __forceinline__ float2 exp2_fma(float2 x) {
-  x.x = max_nan(x.x, -127.0f);
-  x.y = max_nan(x.y, -127.0f);
+  x.x = fmaxf(x.x, -127.0f);
+  x.y = fmaxf(x.y, -127.0f);
   const float2 kShift = make_float2(12582912.0f, 12582912.0f);
   const float2 t = fadd2(x, kShift);
   const float2 f = fadd2(x, fadd2(make_float2(-t.x, -t.y), kShift));
@@ -577,20 +577,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * scale2);
       };
       auto weights = [&](uint32_t (&u)[32], int c, float factor) {
-        float mx4[4];
+        float mx4[4];  // NaN stays
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mx4[k] = fmax3f(__uint_as_float(u[k]), __uint_as_float(u[4 + k]), __uint_as_float(u[8 + k]));
+          mx4[k] =
+              fmax3f_nan(__uint_as_float(u[k]), __uint_as_float(u[4 + k]), __uint_as_float(u[8 + k]));
 #pragma unroll
         for (int i = 12; i < 28; i += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mx4[k] = fmax3f(mx4[k], __uint_as_float(u[i + k]), __uint_as_float(u[i + 4 + k]));
-        const float mx = fmaxf(fmax3f(mx4[0], mx4[1], mx4[2]),
-                               fmax3f(mx4[3], fmax3f(__uint_as_float(u[28]), __uint_as_float(u[29]),
-                                                     __uint_as_float(u[30])),
-                                      __uint_as_float(u[31]))) *
-                         factor;
+            mx4[k] = fmax3f_nan(mx4[k], __uint_as_float(u[i + k]), __uint_as_float(u[i + 4 + k]));
+        const float last4 = fmax3f_nan(
+            mx4[3],
+            fmax3f_nan(__uint_as_float(u[28]), __uint_as_float(u[29]), __uint_as_float(u[30])),
+            __uint_as_float(u[31]));
+        const float mx = max_nan(fmax3f_nan(mx4[0], mx4[1], mx4[2]), last4) * factor;
         uint32_t pk[16];
         float2 cs[4];
         // with the maximum as it stands; once more when these logits move it
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[i] = pack_bf16x2(e.x, e.y);
           }
           if (again) break;
-          const bool grow = mx > m + kRescale || (m == -INFINITY && mx != -INFINITY);
+          const bool grow = mx > m + kRescale || (m == -INFINITY && mx > -INFINITY);
           if (!__any_sync(0xFFFFFFFFu, grow)) break;
           float alpha = 1.0f;
           if (grow) {
@@ -652,6 +653,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        // a row with a logit that is NaN or +infinity: so are its sum and its outputs
+        // (the exponentials on the FMA pipe do not carry a NaN)
+        if (!(mx < INFINITY)) l = __uint_as_float(0x7FC00000u);
 #pragma unroll
         for (int k = 0; k < 4; ++k) sp[k] = fadd2(sp[k], cs[k]);
         tmem_st16(s_tm + static_cast<uint32_t>(16 * c), pk);

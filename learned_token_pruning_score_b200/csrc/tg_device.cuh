@@ -585,6 +585,13 @@ __device__ __forceinline__ float fmax3f(float a, float b, float c) {
   return r;
 }
 
+// The same, and NaN if one of them is.
+__device__ __forceinline__ float fmax3f_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // 2^x on the MUFU unit (ex2.approx: relative error ~2^-22; ex2(-inf) = 0).
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
