@@ -91,19 +91,22 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 // 2^x for a pair on the FMA pipe, x <= 8: x = j + f with j = round(x) (adding
-// 1.5 * 2^23 leaves it in the low mantissa bits), a degree-3 polynomial for
-// 2^f, |f| <= 1/2, fitted here with p(0) = 1 (largest relative error 1.02e-4),
+// 1.5 * 2^23 leaves it in the low mantissa bits), a degree-4 polynomial for
+// 2^f, |f| <= 1/2, fitted here with p(0) = 1 (largest relative error 2.9e-6, a
+// thousandth of what rounding the weight to bf16 takes; of degree 3 1.0e-4),
 // and j added to the exponent field. Below -127 that gives exactly 0, so a
-// masked logit (-inf) has no weight. So does a NaN: its row is marked where the
-// maximum is formed.
+// masked logit (-inf) has no weight; a polynomial with p(0) < 1
+// (exp2_poly3_x2) would leave the exponent's range there. A NaN has no weight
+// either: its row is marked where the maximum is formed.
 __device__ __forceinline__ float2 exp2_fma(float2 x) {
   x.x = fmaxf(x.x, -127.0f);
   x.y = fmaxf(x.y, -127.0f);
   const float2 kShift = make_float2(12582912.0f, 12582912.0f);
   const float2 t = fadd2(x, kShift);
   const float2 f = fadd2(x, fadd2(make_float2(-t.x, -t.y), kShift));
-  float2 p = ffma2(f, make_float2(0.0550089329f, 0.0550089329f), make_float2(0.242210999f, 0.242210999f));
-  p = ffma2(p, f, make_float2(0.693282902f, 0.693282902f));
+  float2 p = ffma2(f, make_float2(0.009585382f, 0.009585382f), make_float2(0.055906627f, 0.055906627f));
+  p = ffma2(p, f, make_float2(0.24024038f, 0.24024038f));
+  p = ffma2(p, f, make_float2(0.6931242f, 0.6931242f));
   p = ffma2(p, f, make_float2(1.0f, 1.0f));
   return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
                      __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
@@ -553,14 +556,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st32_wait(s_tm + static_cast<uint32_t>(c * 32), z);
         }
       }
-      // P = 2^(S scale2 - m), 32 keys at a time, in packed pairs, one pair in four
-      // on the FMA pipe (the MUFU unit is this loop's bottleneck); 32 keys' P covers
-      // 16 columns of logits that have been read. The running maximum m is moved
-      // (to a whole number, so that every rescaling is by an exact power of two)
-      // only when 32 logits pass it by more than 2^8, after their exponentials: no
-      // pass over the row comes before them (2048 tokens after 30720, no bias: 482
-      // us with one, 470 without). What the row has gathered, the P of this tile
-      // included, is rescaled then, and the 32 exponentials are formed again.
+      // P = 2^(S scale2 - m), 32 keys at a time, in packed pairs, three of the 16 pairs
+      // on the FMA pipe (the MUFU unit is this loop's bottleneck; 2048 tokens after
+      // 30720: none 551 us, two 531, these three 516, four 541); 32 keys' P covers 16
+      // columns of logits that have been read. The running maximum m is moved (to a
+      // whole number, so that every rescaling is by an exact power of two) only when 32
+      // logits pass it by more than 2^8, after their exponentials: no pass over the row
+      // comes before them (2048 tokens after 30720, no bias: 482 us with one, 470
+      // without). What the row has gathered, the P of this tile included, is rescaled
+      // then, and the 32 exponentials are formed again.
       float2 sp[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                       make_float2(0.f, 0.f)};
       // The product S scale2 is exact in the FMA, but the maximum comes from the rounded
@@ -603,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 y =
                 ffma2(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), sc2, nm2);
             float2 e;
-            if ((i & 3) == 3) {
+            if (i > 3 && (i & 3) == 3) {
               e = exp2_fma(y);
             } else {
               e.x = ex2_approx(y.x);
