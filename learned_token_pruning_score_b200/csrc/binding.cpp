@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDAStream.h>
 
 #include <algorithm>
+#include <optional>
 #include <string>
 
 #include "tokengate.h"
@@ -67,18 +68,6 @@ int64_t rows3(const Tensor& t, int64_t rows, int64_t heads, int64_t dh, at::Scal
   return rows > 1 ? t.stride(0) : std::max(t.stride(0), heads * dh);
 }
 
-// A given output tensor, or a new one: contiguous, of these sizes.
-Tensor output(PyObject* o, at::IntArrayRef sizes, at::ScalarType type, int64_t index, const char* what) {
-  if (o == Py_None)
-    return at::empty(sizes, at::TensorOptions().dtype(type).device(
-                                c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(index))));
-  const Tensor& t = need_tensor(o, "an output");
-  if (t.sizes() != sizes || t.scalar_type() != type || !t.is_cuda() || t.get_device() != index ||
-      !t.is_contiguous())
-    refuse(what);
-  return t;
-}
-
 tg_dtype dtype_of(const Tensor& t) {
   if (t.scalar_type() == at::kBFloat16) return TG_BF16;
   if (t.scalar_type() == at::kFloat) return TG_F32;
@@ -93,12 +82,42 @@ tg_stream stream_of(PyObject* o, int64_t index) {
   return reinterpret_cast<tg_stream>(PyLong_AsVoidPtr(o));
 }
 
-// What is allocated here belongs to the current stream: where the call runs on
-// another, its memory is not to be handed out again before that one is done.
-void used_on(const Tensor& t, PyObject* stream, tg_stream st, int64_t index) {
-  if (stream != Py_None && t.defined() && t.numel() > 0)
-    t.record_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(st),
-                                                     static_cast<c10::DeviceIndex>(index)));
+// While it lives, what is allocated belongs to the stream of the call: memory
+// of the current stream may still be in use there by what was freed last, which
+// the caller has no reason to wait for. The results go back to a caller on the
+// current stream, so their memory is not to be handed out again before what
+// that stream has been given by then is done.
+class OnStream {
+ public:
+  OnStream(PyObject* stream, tg_stream st, int64_t index) {
+    if (stream == Py_None) return;
+    const auto device = static_cast<c10::DeviceIndex>(index);
+    caller_ = c10::cuda::getCurrentCUDAStream(device);
+    guard_.emplace(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(st), device));
+  }
+  void result(const Tensor& t) const {
+    if (caller_ && t.numel() > 0) t.record_stream(*caller_);
+  }
+
+ private:
+  std::optional<c10::cuda::CUDAStream> caller_;
+  std::optional<c10::cuda::CUDAStreamGuard> guard_;
+};
+
+// A given output tensor, or a new one: contiguous, of these sizes.
+Tensor output(PyObject* o, at::IntArrayRef sizes, at::ScalarType type, int64_t index, const char* what,
+              const OnStream& on) {
+  if (o == Py_None) {
+    Tensor t = at::empty(sizes, at::TensorOptions().dtype(type).device(
+                                    c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(index))));
+    on.result(t);
+    return t;
+  }
+  const Tensor& t = need_tensor(o, "an output");
+  if (t.sizes() != sizes || t.scalar_type() != type || !t.is_cuda() || t.get_device() != index ||
+      !t.is_contiguous())
+    refuse(what);
+  return t;
 }
 
 // Runs the call with the device current; the result, or the status as an int.
@@ -174,6 +193,9 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& v = need_tensor(a[2], "v");
   if (k.dim() != 3) refuse("k must be [rows, heads, head_dim]");
   const int64_t rows = k.size(0), hkv = c.c.n_heads_kv, dh = c.c.head_dim, index = c.index;
+  const tg_stream st = stream_of(a[13], index);
+  if (PyErr_Occurred()) return nullptr;
+  const OnStream on(a[13], st, index);
   const int64_t k_st = rows3(k, rows, hkv, dh, c.type, index, "k");
   const int64_t v_st = rows3(v, rows, hkv, dh, c.type, index, "v");
   const Tensor* q = maybe_tensor(a[5], "q");
@@ -184,7 +206,7 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     hq = q->size(1);
     q_st = rows3(*q, rows, hq, dh, c.type, index, "q");
     out = output(a[12], {rows, hq, dh}, c.type, index,
-                 "q_out must be contiguous, as q in shape and dtype");
+                 "q_out must be contiguous, as q in shape and dtype", on);
   } else if (a[12] != Py_None) {
     refuse("q_out without q");
   }
@@ -195,9 +217,7 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto* qn = vec<float>(maybe_tensor(a[8], "q_norm"), dh, at::kFloat, index, "q_norm");
   const auto* kn = vec<float>(maybe_tensor(a[9], "k_norm"), dh, at::kFloat, index, "k_norm");
   const double eps = PyFloat_AsDouble(a[10]), base = PyFloat_AsDouble(a[11]);
-  const tg_stream st = stream_of(a[13], index);
   if (PyErr_Occurred()) return nullptr;
-  if (a[12] == Py_None) used_on(out, a[13], st, index);
   return finish(
       index,
       [&] {
@@ -218,9 +238,12 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& q = need_tensor(a[1], "q");
   if (q.dim() != 3) refuse("q must be [rows, heads, head_dim]");
   const int64_t rows = q.size(0), hq = q.size(1), dh = c.c.head_dim, index = c.index;
+  const tg_stream st = stream_of(a[10], index);
+  if (PyErr_Occurred()) return nullptr;
+  const OnStream on(a[10], st, index);
   const int64_t q_st = rows3(q, rows, hq, dh, c.type, index, "q");
   Tensor out = output(a[7], {rows, hq, dh}, c.type, index,
-                      "out must be contiguous, as q in shape and dtype");
+                      "out must be contiguous, as q in shape and dtype", on);
   tg_shape shape{};
   shape.n = c.batch;
   shape.k = rows;
@@ -246,10 +269,7 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto* tau = vec<float>(maybe_tensor(a[5], "tau"), hq, at::kFloat, index, "tau");
   const auto* lse = vec<float>(maybe_tensor(a[8], "lse"), hq * rows, at::kFloat, index, "lse");
   const long long max_kv = PyLong_AsLongLong(a[6]);
-  const tg_stream st = stream_of(a[10], index);
   if (PyErr_Occurred()) return nullptr;
-  if (a[7] == Py_None) used_on(out, a[10], st, index);
-  if (a[9] == Py_None) used_on(ws, a[10], st, index);
   return finish(
       index,
       [&] {
@@ -271,12 +291,11 @@ PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t index = cuda_index(x), rows = x.size(0), cols = x.size(1);
   if (x.stride(1) != 1 && rows > 0 && cols > 1) refuse("x: each row must be contiguous");
   const tg_dtype dt = dtype_of(x);
-  Tensor xq = output(a[1], {rows, cols}, at::kChar, index, "xq must be contiguous int8 of x's shape");
-  Tensor scale = output(a[2], {rows}, at::kFloat, index, "scale must be contiguous fp32 [rows]");
   const tg_stream st = stream_of(a[3], index);
   if (PyErr_Occurred()) return nullptr;
-  if (a[1] == Py_None) used_on(xq, a[3], st, index);
-  if (a[2] == Py_None) used_on(scale, a[3], st, index);
+  const OnStream on(a[3], st, index);
+  Tensor xq = output(a[1], {rows, cols}, at::kChar, index, "xq must be contiguous int8 of x's shape", on);
+  Tensor scale = output(a[2], {rows}, at::kFloat, index, "scale must be contiguous fp32 [rows]", on);
   return finish(
       index,
       [&] {
@@ -301,7 +320,10 @@ PyObject* linear_quantized(PyObject*, PyObject* const* a, Py_ssize_t n) {
     refuse("xq [m, k] and wq [n, k] must be contiguous int8 on one device");
   const Tensor* given = maybe_tensor(a[5], "y");
   const at::ScalarType type = given ? given->scalar_type() : a[6] == Py_True ? at::kFloat : at::kBFloat16;
-  Tensor y = output(a[5], {m, cols}, type, index, "y must be contiguous [m, n] on xq's device");
+  const tg_stream st = stream_of(a[7], index);
+  if (PyErr_Occurred()) return nullptr;
+  const OnStream on(a[7], st, index);
+  Tensor y = output(a[5], {m, cols}, type, index, "y must be contiguous [m, n] on xq's device", on);
   const tg_dtype dt = dtype_of(y);
   const Tensor* res = maybe_tensor(a[4], "residual");
   if (res != nullptr && (res->sizes() != y.sizes() || res->scalar_type() != type || !res->is_cuda() ||
@@ -309,9 +331,6 @@ PyObject* linear_quantized(PyObject*, PyObject* const* a, Py_ssize_t n) {
     refuse("residual must be contiguous [m, n], as y");
   const auto* xs = vec<float>(&need_tensor(a[1], "xs"), m, at::kFloat, index, "xs");
   const auto* ws = vec<float>(&need_tensor(a[3], "ws"), cols, at::kFloat, index, "ws");
-  const tg_stream st = stream_of(a[7], index);
-  if (PyErr_Occurred()) return nullptr;
-  if (given == nullptr) used_on(y, a[7], st, index);
   return finish(
       index,
       [&] {
