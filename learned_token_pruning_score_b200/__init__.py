@@ -705,6 +705,7 @@ class PagedKV:
             _need(n_pages == 0 or t[0].is_contiguous(), f"{name}: each page must be contiguous")
         _need(table.dim() == 2 and table.dtype == torch.int32 and table.is_contiguous()
               and table.device == k.device, "table must be a contiguous int32 [batch, max_pages]")
+        _need(max(k.shape + table.shape) < 2 ** 31, "sizes of the pages and the table must be below 2^31")
         if bias is not None:
             _need(bias.dtype == torch.float32 and bias.shape == (n_pages, ps)
                   and bias.device == k.device and (ps == 1 or bias.stride(1) == 1),

@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDAStream.h>
 
 #include <algorithm>
+#include <cstdint>
 #include <optional>
 #include <string>
 
@@ -34,6 +35,12 @@ const Tensor& need_tensor(PyObject* o, const char* name) {
 // None: no tensor
 const Tensor* maybe_tensor(PyObject* o, const char* name) {
   return o == Py_None ? nullptr : &need_tensor(o, name);
+}
+
+// Sizes that the C ABI holds in 32 bits.
+int32_t int32_of(int64_t n, const char* name) {
+  if (n > INT32_MAX) refuse(std::string(name) + " " + std::to_string(n) + " is above 2^31 - 1");
+  return static_cast<int32_t>(n);
 }
 
 std::string at_device(int64_t index) { return " on cuda:" + std::to_string(index); }
@@ -155,7 +162,8 @@ bool arity(Py_ssize_t have, Py_ssize_t want) {
 // ------------------------------------------------------------------ cache
 struct Cache {
   tg_paged_kv c;
-  int64_t index, batch;
+  int64_t index;
+  int32_t batch;
   at::ScalarType type;
 };
 constexpr const char* kCache = "tokengate.paged_kv";
@@ -170,7 +178,7 @@ PyObject* make_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const long index = PyLong_AsLong(a[1]);
   const long long batch = PyLong_AsLongLong(a[2]);
   if (PyErr_Occurred()) return nullptr;
-  auto* k = new Cache{*c, index, batch, c->dtype == TG_BF16 ? at::kBFloat16 : at::kFloat};
+  auto* k = new Cache{*c, index, int32_of(batch, "the table's batch"), c->dtype == TG_BF16 ? at::kBFloat16 : at::kFloat};
   PyObject* o = PyCapsule_New(k, kCache, free_cache);
   if (o == nullptr) delete k;
   return o;
@@ -199,18 +207,19 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t k_st = rows3(k, rows, hkv, dh, c.type, index, "k");
   const int64_t v_st = rows3(v, rows, hkv, dh, c.type, index, "v");
   const Tensor* q = maybe_tensor(a[5], "q");
-  int64_t hq = 0, q_st = 0;
+  int32_t hq = 0;
+  int64_t q_st = 0;
   Tensor out;
   if (q != nullptr) {
     if (q->dim() != 3) refuse("q must be [rows, heads, head_dim]");
-    hq = q->size(1);
+    hq = int32_of(q->size(1), "q's heads");
     q_st = rows3(*q, rows, hq, dh, c.type, index, "q");
     out = output(a[12], {rows, hq, dh}, c.type, index,
                  "q_out must be contiguous, as q in shape and dtype", on);
   } else if (a[12] != Py_None) {
     refuse("q_out without q");
   }
-  const auto* cu = vec<int32_t>(&need_tensor(a[3], "cu_q"), c.batch + 1, at::kInt, index, "cu_q");
+  const auto* cu = vec<int32_t>(&need_tensor(a[3], "cu_q"), int64_t(c.batch) + 1, at::kInt, index, "cu_q");
   const auto* len = vec<int32_t>(&need_tensor(a[4], "kv_len"), c.batch, at::kInt, index, "kv_len");
   const auto* pos = vec<int32_t>(maybe_tensor(a[6], "pos"), rows, at::kInt, index, "pos");
   const auto* s = vec<float>(maybe_tensor(a[7], "s"), rows, at::kFloat, index, "s");
@@ -222,8 +231,7 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       index,
       [&] {
         return tg_paged_append(&c.c, q ? q->data_ptr() : nullptr, q_st, k.data_ptr(), k_st, v.data_ptr(),
-                               v_st, rows, cu, len, static_cast<int32_t>(c.batch),
-                               static_cast<int32_t>(hq), pos, s, qn, kn, static_cast<float>(eps),
+                               v_st, rows, cu, len, c.batch, hq, pos, s, qn, kn, static_cast<float>(eps),
                                static_cast<float>(base), q ? out.data_ptr() : nullptr, st);
       },
       wrap_one, q ? &out : nullptr, nullptr);
@@ -237,7 +245,8 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Cache& c = cache_of(a[0]);
   const Tensor& q = need_tensor(a[1], "q");
   if (q.dim() != 3) refuse("q must be [rows, heads, head_dim]");
-  const int64_t rows = q.size(0), hq = q.size(1), dh = c.c.head_dim, index = c.index;
+  const int32_t hq = int32_of(q.size(1), "q's heads");
+  const int64_t rows = q.size(0), dh = c.c.head_dim, index = c.index;
   const tg_stream st = stream_of(a[10], index);
   if (PyErr_Occurred()) return nullptr;
   const OnStream on(a[10], st, index);
@@ -247,7 +256,7 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   tg_shape shape{};
   shape.n = c.batch;
   shape.k = rows;
-  shape.n_heads_q = static_cast<int32_t>(hq);
+  shape.n_heads_q = hq;
   shape.n_heads_kv = c.c.n_heads_kv;
   shape.head_dim = c.c.head_dim;
   shape.dtype = c.c.dtype;
@@ -263,7 +272,7 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   } else if (need > 0) {
     ws = at::empty({need}, q.options().dtype(at::kByte));
   }
-  const auto* cu = vec<int32_t>(&need_tensor(a[2], "cu_q"), c.batch + 1, at::kInt, index, "cu_q");
+  const auto* cu = vec<int32_t>(&need_tensor(a[2], "cu_q"), int64_t(c.batch) + 1, at::kInt, index, "cu_q");
   const auto* len = vec<int32_t>(&need_tensor(a[3], "kv_len"), c.batch, at::kInt, index, "kv_len");
   const auto* gain = vec<float>(maybe_tensor(a[4], "gain"), hq, at::kFloat, index, "gain");
   const auto* tau = vec<float>(maybe_tensor(a[5], "tau"), hq, at::kFloat, index, "tau");
@@ -273,8 +282,7 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return finish(
       index,
       [&] {
-        return tg_paged_attn(&c.c, q.data_ptr(), q_st, rows, cu, len, static_cast<int32_t>(c.batch),
-                             static_cast<int32_t>(hq), max_kv, gain, tau, out.data_ptr(),
+        return tg_paged_attn(&c.c, q.data_ptr(), q_st, rows, cu, len, c.batch, hq, max_kv, gain, tau, out.data_ptr(),
                              const_cast<float*>(lse), ws.defined() ? ws.data_ptr() : nullptr,
                              ws.defined() ? size_t(ws.numel()) * ws.element_size() : 0, st);
       },
@@ -288,7 +296,8 @@ PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!arity(n, 4)) return nullptr;
   const Tensor& x = need_tensor(a[0], "x");
   if (x.dim() != 2) refuse("x must be [rows, cols]");
-  const int64_t index = cuda_index(x), rows = x.size(0), cols = x.size(1);
+  const int32_t cols = int32_of(x.size(1), "x's columns");
+  const int64_t index = cuda_index(x), rows = x.size(0);
   if (x.stride(1) != 1 && rows > 0 && cols > 1) refuse("x: each row must be contiguous");
   const tg_dtype dt = dtype_of(x);
   const tg_stream st = stream_of(a[3], index);
@@ -300,7 +309,7 @@ PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
       index,
       [&] {
         return tg_quantize_rows(x.data_ptr(), rows > 1 ? x.stride(0) : cols, rows,
-                                static_cast<int32_t>(cols), dt, static_cast<int8_t*>(xq.data_ptr()),
+                                cols, dt, static_cast<int8_t*>(xq.data_ptr()),
                                 static_cast<float*>(scale.data_ptr()), st);
       },
       wrap_two, &xq, &scale);
@@ -314,7 +323,8 @@ PyObject* linear_quantized(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& xq = need_tensor(a[0], "xq");
   const Tensor& wq = need_tensor(a[2], "wq");
   if (xq.dim() != 2 || wq.dim() != 2) refuse("xq must be [m, k], wq [n, k]");
-  const int64_t index = cuda_index(xq), m = xq.size(0), k = xq.size(1), cols = wq.size(0);
+  const int32_t k = int32_of(xq.size(1), "k"), cols = int32_of(wq.size(0), "n");
+  const int64_t index = cuda_index(xq), m = xq.size(0);
   if (wq.size(1) != k || xq.scalar_type() != at::kChar || wq.scalar_type() != at::kChar ||
       !wq.is_cuda() || wq.get_device() != index || !xq.is_contiguous() || !wq.is_contiguous())
     refuse("xq [m, k] and wq [n, k] must be contiguous int8 on one device");
@@ -336,8 +346,7 @@ PyObject* linear_quantized(PyObject*, PyObject* const* a, Py_ssize_t n) {
       [&] {
         return tg_linear_quantized(static_cast<const int8_t*>(xq.data_ptr()), xs,
                                    static_cast<const int8_t*>(wq.data_ptr()), ws,
-                                   res ? res->data_ptr() : nullptr, m, static_cast<int32_t>(cols),
-                                   static_cast<int32_t>(k), dt, y.data_ptr(), st);
+                                   res ? res->data_ptr() : nullptr, m, cols, k, dt, y.data_ptr(), st);
       },
       wrap_one, &y, nullptr);
   END_HANDLE_TH_ERRORS
