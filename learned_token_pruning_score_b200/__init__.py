@@ -694,7 +694,9 @@ class PagedKV:
     (bf16 or fp32; a page must be contiguous, pages may be apart, so a layer
     of a pool [n_pages, n_layers, ...] will do), table [batch, max_pages]
     int32 (page of each block of page_size rows of a request) and optionally
-    bias [n_pages, page_size] fp32 (gate biases logsigmoid(s), 0 = none)."""
+    bias [n_pages, page_size] fp32 (gate biases logsigmoid(s), 0 = none). It
+    keeps to these tensors: what they hold may change from call to call, but a
+    larger table, or other pages, are another PagedKV."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
                  bias: Optional[torch.Tensor] = None):
@@ -710,21 +712,23 @@ class PagedKV:
             _need(bias.dtype == torch.float32 and bias.shape == (n_pages, ps)
                   and bias.device == k.device and (ps == 1 or bias.stride(1) == 1),
                   "bias must be fp32 [n_pages, page_size]")
-        self.k, self.v, self.table, self.bias = k, v, table, bias
-        self.page_size, self.n_heads_kv, self.head_dim = ps, hkv, dh
-        self.dtype, self.device = k.dtype, k.device
-        self.batch = table.shape[0]
-        self.capacity = table.shape[1] * ps  # rows that the table has room for, per request
         page = ps * hkv * dh
 
         def apart(t, least):
             return t.stride(0) if n_pages > 1 else max(t.stride(0), least)
 
-        self.c = TgPagedKv(k.data_ptr(), v.data_ptr(), None if bias is None else bias.data_ptr(),
-                           table.data_ptr(), n_pages, apart(k, page), apart(v, page),
-                           0 if bias is None else apart(bias, ps), table.shape[1], ps, hkv, dh,
-                           _dt(k))
-        self._h = _binding.cache(ctypes.addressof(self.c), k.get_device(), self.batch)
+        c = TgPagedKv(k.data_ptr(), v.data_ptr(), None if bias is None else bias.data_ptr(),
+                      table.data_ptr(), n_pages, apart(k, page), apart(v, page),
+                      0 if bias is None else apart(bias, ps), table.shape[1], ps, hkv, dh, _dt(k))
+        self.__dict__.update(
+            k=k, v=v, table=table, bias=bias, page_size=ps, n_heads_kv=hkv, head_dim=dh,
+            dtype=k.dtype, device=k.device, batch=table.shape[0],
+            capacity=table.shape[1] * ps,  # rows that the table has room for, per request
+            c=c, _h=_binding.cache(ctypes.addressof(c), k.get_device(), table.shape[0], k, v, table,
+                                   bias))
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a PagedKV keeps to the tensors that it was made of; make another one")
 
 
 def tg_paged_append(cache: PagedKV, k, v, cu_q, kv_len, q=None, pos=None, s=None, q_norm=None,

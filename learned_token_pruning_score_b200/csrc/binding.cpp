@@ -165,20 +165,24 @@ struct Cache {
   int64_t index;
   int32_t batch;
   at::ScalarType type;
+  Tensor k, v, table, bias;  // the memory that c points at
 };
 constexpr const char* kCache = "tokengate.paged_kv";
 
 void free_cache(PyObject* o) { delete static_cast<Cache*>(PyCapsule_GetPointer(o, kCache)); }
 
-// cache(address of a tg_paged_kv, device index, batch): a copy of it for the calls
+// cache(address of a tg_paged_kv, device index, batch, k, v, table, bias or None): a
+// copy of it for the calls, which keeps the tensors
 PyObject* make_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (!arity(n, 3)) return nullptr;
+  if (!arity(n, 7)) return nullptr;
   const auto* c = static_cast<const tg_paged_kv*>(PyLong_AsVoidPtr(a[0]));
   const long index = PyLong_AsLong(a[1]);
   const long long batch = PyLong_AsLongLong(a[2]);
   if (PyErr_Occurred()) return nullptr;
-  auto* k = new Cache{*c, index, int32_of(batch, "the table's batch"), c->dtype == TG_BF16 ? at::kBFloat16 : at::kFloat};
+  auto* k = new Cache{*c, index, int32_of(batch, "the table's batch"), c->dtype == TG_BF16 ? at::kBFloat16 : at::kFloat,
+                      need_tensor(a[3], "k"), need_tensor(a[4], "v"), need_tensor(a[5], "table"),
+                      a[6] == Py_None ? Tensor() : need_tensor(a[6], "bias")};
   PyObject* o = PyCapsule_New(k, kCache, free_cache);
   if (o == nullptr) delete k;
   return o;

@@ -26,3 +26,21 @@ def test_sizes_beyond_32_bits_are_refused():
                      (torch.empty(0, BIG + 16, 2, 64), torch.empty(1, 1, dtype=torch.int32))):
         with pytest.raises(ValueError, match="below 2\\^31"):
             tg.PagedKV(k, k, table)
+
+
+def test_a_cache_keeps_to_its_tensors():
+    """A table that has grown is another cache: the calls would go on with the
+    old one's memory. The handle that they get keeps that memory."""
+    k, table = torch.zeros(4, 16, 2, 64), torch.zeros(2, 2, dtype=torch.int32)
+    v, bias = torch.zeros_like(k), torch.zeros(4, 16)
+    held = [t._use_count() for t in (k, v, table, bias)]
+    c = tg.PagedKV(k, v, table, bias)
+    for name in ("k", "v", "table", "bias", "capacity", "page_size", "batch", "c"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, getattr(c, name))
+    assert c.table is table and c.capacity == 32 and c.bias is bias
+    handle = c._h
+    del c
+    assert [t._use_count() for t in (k, v, table, bias)] == [n + 1 for n in held]
+    del handle
+    assert [t._use_count() for t in (k, v, table, bias)] == held
