@@ -80,28 +80,46 @@ def build(verbose: bool = False, force: bool = False) -> str:
     return LIB
 
 
+CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-shared", "-DNDEBUG"]
+BINDING_LIBS = ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
 def build_binding(verbose: bool = False, force: bool = False) -> str:
+    """Builds _binding.so when its sources, or what its binary interface comes
+    from (torch, Python, the compiler and its flags), are not those it was
+    built from; the latter stand in a stamp beside the objects."""
     import sysconfig
 
     import torch
 
     src = os.path.join(CSRC, "binding.cpp")
-    if not force and not _newer(src, BINDING, [LIB, os.path.join(INCLUDE, "tokengate.h")]):
+    cxx = os.environ.get("CXX", "g++")
+    abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    made_for = "\n".join([f"torch {torch.__version__}", f"python {sys.version}",
+                          " ".join([cxx, *CXX_FLAGS, abi, *BINDING_LIBS])])
+    stamp = os.path.join(BUILD, "binding.stamp")
+    same = False
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            same = f.read() == made_for
+    if (same and not force
+            and not _newer(src, BINDING, [LIB, os.path.join(INCLUDE, "tokengate.h")])):
         return BINDING
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-DNDEBUG",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           *[a for i in inc for a in ("-isystem", i)], src, "-o", BINDING,
-           "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+    cmd = [cxx, *CXX_FLAGS, abi, *[a for i in inc for a in ("-isystem", i)], src, "-o", BINDING,
+           "-L" + os.path.join(root, "lib"), *BINDING_LIBS,
            "-L" + HERE, "-l:libtokengate.so", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"binding failed:\n{r.stdout}\n{r.stderr}")
+    os.makedirs(BUILD, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(made_for)
     return BINDING
 
 

@@ -44,3 +44,30 @@ def test_a_cache_keeps_to_its_tensors():
     assert [t._use_count() for t in (k, v, table, bias)] == [n + 1 for n in held]
     del handle
     assert [t._use_count() for t in (k, v, table, bias)] == held
+
+
+def test_the_module_is_rebuilt_for_another_torch(monkeypatch, tmp_path):
+    """What the module's binary interface comes from is part of the check that
+    finds it up to date."""
+    from learned_token_pruning_score_b200 import _build
+
+    runs = []
+
+    class Done:
+        returncode, stdout, stderr = 0, "", ""
+
+    monkeypatch.setattr(_build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(_build, "_newer", lambda *a: False)
+    monkeypatch.setattr(_build.subprocess, "run", lambda cmd, **kw: runs.append(cmd) or Done())
+    _build.build_binding()
+    assert len(runs) == 1  # no stamp
+    _build.build_binding()
+    assert len(runs) == 1  # up to date
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    _build.build_binding()
+    _build.build_binding()
+    assert len(runs) == 2
+    monkeypatch.setattr(_build, "CXX_FLAGS", [*_build.CXX_FLAGS, "-g"])
+    _build.build_binding()
+    _build.build_binding(force=True)
+    assert len(runs) == 4
