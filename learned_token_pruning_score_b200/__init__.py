@@ -12,6 +12,8 @@ it raises ImportError -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 from dataclasses import dataclass
 from typing import Dict, List, Optional, Sequence
@@ -187,10 +189,48 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return t.data_ptr()
 
 
-def _stream(stream, device) -> Optional[int]:
+def _handle(stream) -> Optional[int]:
+    """A stream's handle (None: the current stream)."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        return None
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _stream(stream, device) -> Optional[int]:
+    return _handle(torch.cuda.current_stream(device) if stream is None else stream)
+
+
+def _on_its_stream(call):
+    """The call with its stream current, where it is given another one: what it
+    allocates then belongs to that stream (memory of the current one may still
+    be in use there), and its results are kept until the current stream, on
+    which they go back to the caller, is done with them."""
+    at = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def run(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return call(*args, **kw)
+        handle = _handle(stream)
+        device = next((t.device for t in (*args, *kw.values())
+                       if isinstance(t, torch.Tensor) and t.is_cuda), getattr(stream, "device", None))
+        caller = torch.cuda.current_stream(device)
+        if handle == caller.cuda_stream:
+            return call(*args, **kw)
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle, caller.device) if handle
+                               else torch.cuda.default_stream(caller.device)):
+            results = call(*args, **kw)
+        todo = [results]
+        while todo:
+            r = todo.pop()
+            if isinstance(r, (tuple, list)):
+                todo.extend(r)
+            elif isinstance(r, torch.Tensor) and r.is_cuda:
+                r.record_stream(caller)
+        return results
+
+    return run
 
 
 def _ws(nbytes: int, device, ws: Optional[torch.Tensor]) -> torch.Tensor:
@@ -255,6 +295,7 @@ def tg_trace_stop() -> List[dict]:
 # ----------------------------------------------------------------- the calls
 
 
+@_on_its_stream
 def tg_score(x, norm_w, w1, w2, b1=None, b2=None, eps: float = 1e-6, scores=None, ws=None,
              stream=None) -> torch.Tensor:
     n, d = x.shape
@@ -269,6 +310,7 @@ def tg_score(x, norm_w, w1, w2, b1=None, b2=None, eps: float = 1e-6, scores=None
     return scores
 
 
+@_on_its_stream
 def tg_topk_select(scores, protect, k: int, kept_idx=None, ws=None, stream=None) -> torch.Tensor:
     n = scores.shape[0]
     if kept_idx is None:
@@ -280,6 +322,7 @@ def tg_topk_select(scores, protect, k: int, kept_idx=None, ws=None, stream=None)
     return kept_idx
 
 
+@_on_its_stream
 def tg_linear(x, w, residual=None, y=None, stream=None) -> torch.Tensor:
     """y = x . w^T (+ residual): x [m, k], w [n, k] (nn.Linear layout)."""
     m, k = x.shape
@@ -291,6 +334,7 @@ def tg_linear(x, w, residual=None, y=None, stream=None) -> torch.Tensor:
     return y
 
 
+@_on_its_stream
 def tg_fold_norm_weight(w, g, out=None, stream=None) -> torch.Tensor:
     """W_g = bf16(W . diag(g)): w [rows, cols] bf16, g [cols] fp32 (the weight
     of the RMSNorm in front of the projection w)."""
@@ -305,6 +349,7 @@ def tg_fold_norm_weight(w, g, out=None, stream=None) -> torch.Tensor:
 SELECT_NOALLOC_MAX_N = 1 << 20
 
 
+@_on_its_stream
 def tg_topk_select_noalloc(scores, protect, k: int, kept_idx=None, stream=None) -> torch.Tensor:
     """tg_topk_select with no workspace: the library keeps this call's scratch
     in a static device array (n <= SELECT_NOALLOC_MAX_N). For callers that can
@@ -321,6 +366,7 @@ def tg_topk_select_noalloc(scores, protect, k: int, kept_idx=None, stream=None) 
     return kept_idx
 
 
+@_on_its_stream
 def tg_compact(x, kept_idx, pos_in=None, scores=None, x_out=None, pos_out=None, scores_out=None,
                stream=None):
     n, d = x.shape
@@ -337,6 +383,7 @@ def tg_compact(x, kept_idx, pos_in=None, scores=None, x_out=None, pos_out=None, 
     return x_out, pos_out, scores_out
 
 
+@_on_its_stream
 def tg_gated_attn_prefill(q, k, v, pos, s=None, gain=None, tau=None, rope_base: float = 1e6,
                           out=None, ws=None, stream=None) -> torch.Tensor:
     t, hq, dh = q.shape
@@ -353,6 +400,7 @@ def tg_gated_attn_prefill(q, k, v, pos, s=None, gain=None, tau=None, rope_base: 
     return out
 
 
+@_on_its_stream
 def tg_gated_attn_forward(q, k, v, pos, s=None, gain=None, tau=None, rope_base: float = 1e6,
                           out=None, lse=None, out_f32=None, want_f32: bool = True, ws=None,
                           stream=None):
@@ -377,6 +425,7 @@ def tg_gated_attn_forward(q, k, v, pos, s=None, gain=None, tau=None, rope_base: 
     return out, lse, out_f32
 
 
+@_on_its_stream
 def tg_gated_attn_backward(q, k, v, pos, out, lse, dout, s=None, gain=None, tau=None,
                            rope_base: float = 1e6, out_f32=None, dq=None, dk=None, dv=None,
                            ds=None, dgain=None, dtau=None, want_ds: bool = True, ws=None,
@@ -431,6 +480,7 @@ def tg_gated_deltanet_workspace_size(layer: GdnLayer, T: int) -> int:
     return int(_gdn_ws(ctypes.byref(layer.c), T))
 
 
+@_on_its_stream
 def tg_gated_deltanet(layer: GdnLayer, qkv, z, a, b, conv_in=None, state_in=None,
                       want_state: bool = True, y=None, conv_out=None, state_out=None, ws=None,
                       stream=None):
@@ -528,6 +578,7 @@ class Model:
         return int(_prefill_ws(ctypes.byref(self.c), n, k))
 
 
+@_on_its_stream
 def tg_decode_step(model: Model, x, pos: int, gate_layer: int, kv: Sequence, lens: Sequence[int],
                    scores=None, kept_idx=None, out=None, ws=None, stream=None):
     """One generated token through every layer after a gated prefill.
@@ -553,6 +604,7 @@ def tg_decode_step(model: Model, x, pos: int, gate_layer: int, kv: Sequence, len
     return out
 
 
+@_on_its_stream
 def tg_prefill_host(model: Model, x_host, protect, k: int, gate_layer: int, device=None,
                     out=None, kept_idx=None, scores=None, kv: Optional[Sequence] = None, ws=None,
                     stream=None):
@@ -581,6 +633,7 @@ def tg_prefill_host(model: Model, x_host, protect, k: int, gate_layer: int, devi
     return out, kept_idx, scores
 
 
+@_on_its_stream
 def tg_prefill(model: Model, x, protect, k: int, gate_layer: int, out=None, kept_idx=None,
                scores=None, kv: Optional[Sequence] = None, taps: Optional[Sequence] = None,
                ws=None, stream=None):
@@ -619,6 +672,7 @@ def tg_prefill(model: Model, x, protect, k: int, gate_layer: int, out=None, kept
     return out, kept_idx, scores
 
 
+@_on_its_stream
 def tg_prefill_multi(model: Model, x, protect, ks: Sequence[int], gate_layer: int, outs=None,
                      kept_idx=None, scores=None, ws=None, stream=None):
     """The gated prefill at several budgets of one request: the layers below
@@ -640,6 +694,7 @@ def tg_prefill_multi(model: Model, x, protect, ks: Sequence[int], gate_layer: in
     return outs, kept_idx, scores
 
 
+@_on_its_stream
 def tg_prefill_batch(model: Model, x, protect, lens: Sequence[int], ks: Sequence[int],
                      gate_layer: int, out=None, kept_idx=None, scores=None, ws=None, stream=None):
     """The gated prefill of len(lens) requests packed back to back in x
@@ -675,13 +730,6 @@ def tg_prefill_batch(model: Model, x, protect, lens: Sequence[int], ks: Sequence
 # These calls are made once a layer and token, where the kernels take a few
 # microseconds; their checks, allocations and the call of the ABI are in the
 # extension module (csrc/binding.cpp).
-
-
-def _handle(stream):
-    """A stream as the extension takes it: None or its handle."""
-    if stream is None:
-        return None
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _need(cond: bool, what: str) -> None:
