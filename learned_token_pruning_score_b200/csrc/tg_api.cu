@@ -2046,6 +2046,7 @@ tg_status tg_paged_attn(const tg_paged_kv* cache, const void* q, int64_t q_strid
            TG_ERR_INVALID_ARG);
   TG_CHECK(rows * hq < (int64_t(1) << 31) && max_kv <= (int64_t(1) << 30), TG_ERR_UNSUPPORTED);
   if (none) return TG_OK;
+  if (gain == nullptr) a.kv.bias = nullptr;  // no bias: what the cache holds there is not read
   a.q = q;
   a.q_stride = q_stride;
   a.rows = rows;
