@@ -602,10 +602,11 @@ tg_status tg_paged_append(const tg_paged_kv* cache, const void* q, int64_t q_str
  *     reported); at most table_stride page_size. It only has to hold, but a
  *     close one lets the call size its launch closely.
  *   out [rows, hq, dh] dtype; lse [hq, rows] fp32 or NULL: log sum_j exp(l_ij)
- * A logit of -inf, or below -1e30 (log2 units), such as that of a bias of
- * -inf, removes the key; a row that has no key left (or kv_len[b] < n_b)
- * gets zeros and lse -inf. Values of keys that a row does not see never reach
- * it, whatever they hold. The chunk's own rows must be in the cache
+ * A gate bias below -1e20 that takes the logit below -1e30 (log2 units), such
+ * as one of -inf with a gain above 1e-8, removes the key; a row that has no key
+ * left (or kv_len[b] < n_b) gets zeros and lse -inf. Any other logit counts,
+ * however low. Values of keys that a row does not see never reach it, whatever
+ * they hold. The chunk's own rows must be in the cache
  * (tg_paged_append). rows x hq < 2^31 and max_kv <= 2^30 (else
  * TG_ERR_UNSUPPORTED).
  * Workspace: tg_workspace_size(TG_OP_PAGED_ATTN) with

@@ -452,8 +452,9 @@ __global__ void __launch_bounds__(kSimtThreads)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j = kv0 + tx + 8 * i;
-        const float z = s[r][i] * scale[r] + gain[r] * sm.bias[st][tx + 8 * i];
-        seen[i] = j < limit[r] && j < kv_end && !(z <= kMaskedLogit);
+        const float b = sm.bias[st][tx + 8 * i];
+        const float z = s[r][i] * scale[r] + gain[r] * b;
+        seen[i] = j < limit[r] && j < kv_end && !(b < kRemovableBias && z <= kMaskedLogit);
         all = all && seen[i];
         s[r][i] = seen[i] ? z : -INFINITY;
         mx = fmaxf(mx, s[r][i]);

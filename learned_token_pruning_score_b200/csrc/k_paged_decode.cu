@@ -286,6 +286,14 @@ __global__ void __launch_bounds__(kThreads, 2)
           sc[t][2] = fmaf(gain2[1], b.x, sc[t][2] * scale[1]);
           sc[t][3] = fmaf(gain2[1], b.y, sc[t][3] * scale[1]);
         }
+        if (partial != 0) {  // keys that their bias may remove
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (((partial >> (t * 8 + (lane & 3) * 2 + (e & 1))) & 1u) && sc[t][e] <= kMaskedLogit)
+                sc[t][e] = -INFINITY;
+        }
       } else {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -302,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int j = j0 + t * 8 + (lane & 3) * 2 + (e & 1);
-            if (j >= limit[e >> 1] || j >= hi || sc[t][e] <= kMaskedLogit) sc[t][e] = -INFINITY;
+            if (j >= limit[e >> 1] || j >= hi) sc[t][e] = -INFINITY;
           }
       }
       float mx[2];

@@ -9,14 +9,15 @@ namespace tg {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// Logits (log2 units) at or below this count as masked: the weight is zero
-// even where a row has no other key. Gate biases are held above -1e38, so
-// that a bias of -inf (or of the type's lowest value) times a zero gain is
-// zero and not NaN; times any gain above 1e-8 it lands below this bound.
+// A key is removed by its gate bias: where the bias is below kRemovableBias and
+// the logit (log2 units) at or below kMaskedLogit, the weight is zero even if a
+// row has no other key. (The kernels look at a block's logits one by one when it
+// holds such a bias. A logit that the product alone takes so far down is one
+// like any other.) Gate biases are held above -1e38, so that a bias of -inf (or
+// of the type's lowest value) times a zero gain is zero and not NaN; times any
+// gain above 1e-8 it lands below the bound.
 constexpr float kMaskedLogit = -1e30f;
 constexpr float kLowestBias = -1e38f;
-// Only keys with a bias below this one can be removed by it (gains up to
-// 1e10): the kernels look at a block's logits one by one when it holds some.
 constexpr float kRemovableBias = -1e20f;
 
 __device__ __forceinline__ float key_bias(float b) { return b < kLowestBias ? kLowestBias : b; }
