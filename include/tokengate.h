@@ -729,6 +729,8 @@ typedef struct {
   float ms;        /* device time between the bracketing events             */
   double flops;    /* algorithmic FLOPs of the launch (0 if memory-bound)   */
   double bytes;    /* algorithmic bytes of the launch                       */
+  /* (tg_paged_attn: its lengths are device data, and both are bounds: every
+   * row sees max_kv keys, min(rows, batch) requests have as many)          */
 } tg_trace_record;
 
 /* Starts tracing on this host thread, for at most `capacity` launches. */

@@ -2062,9 +2062,13 @@ tg_status tg_paged_attn(const tg_paged_kv* cache, const void* q, int64_t q_strid
   a.err = device_error_word();
   TG_CHECK(ws != nullptr && ws_bytes >= paged_attn_ws_bytes(rows, hq, dh), TG_ERR_WORKSPACE);
   TG_CHECK(aligned16(ws), TG_ERR_INVALID_ARG);
-  const double bytes = 2.0 * rows * hq * dh * double(elem_size(dt));
+  // the lengths are device data: every request that may have rows counts with max_kv keys
+  const double keys = double(std::min<int64_t>(rows, batch)) * max_kv;
+  const double flops = 4.0 * dh * hq * double(rows) * max_kv;
+  const double bytes = 2.0 * rows * hq * dh * double(elem_size(dt)) +
+                       keys * (2.0 * hkv * dh * double(elem_size(dt)) + (a.kv.bias ? 4.0 : 0.0));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return cuda_status(traced(TG_K_PAGED_ATTN, rows, 0.0, bytes, st, [&] {
+  return cuda_status(traced(TG_K_PAGED_ATTN, rows, flops, bytes, st, [&] {
     if (dt == TG_F32) return launch_paged_attn_simt(a, ws, st);
     return paged_tile_rows(rows, batch, hq, hkv) == 16 ? launch_paged_decode(a, ws, st)
                                                        : launch_paged_tc(a, ws, st);
@@ -2098,7 +2102,9 @@ tg_status tg_linear_quantized(const int8_t* xq, const float* xs, const int8_t* w
            TG_ERR_INVALID_ARG);
   const QuantGemmArgs g{xq, xs, wq, ws, residual, y, m, n, k, dt == TG_BF16};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return cuda_status(traced(TG_K_GEMM_INT, m, 2.0 * m * n * k, 0.0, st, [&] {
+  const double bytes = double(m + n) * (k + 4.0) +
+                       double(m) * n * double(elem_size(dt)) * (residual != nullptr ? 2.0 : 1.0);
+  return cuda_status(traced(TG_K_GEMM_INT, m, 2.0 * m * n * k, bytes, st, [&] {
     return launch_quant_gemm(g, st);
   }));
 }
