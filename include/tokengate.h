@@ -572,7 +572,8 @@ typedef struct {
  *   pos [rows] int32: the original positions, or NULL: row index kv_len[b] -
  *     n_b + i of the request.
  *   s [rows] fp32: gate scores of kept rows (bias logsigmoid(s)), or NULL
- *     (bias 0). Unused when the cache holds no bias.
+ *     (bias 0). Generated rows in a call with kept ones have s = +inf, whose
+ *     bias is 0. Unused when the cache holds no bias.
  *   q_norm, k_norm [dh] fp32 or NULL (each on its own), eps: y = x /
  *     sqrt(mean(x^2) + eps) * w per head.
  *   rope_base > 0, or 0: no rotation (keys that are rotated already, such as
@@ -611,8 +612,13 @@ tg_status tg_paged_append(const tg_paged_kv* cache, const void* q, int64_t q_str
  * TG_ERR_UNSUPPORTED).
  * Workspace: tg_workspace_size(TG_OP_PAGED_ATTN) with
  * n = batch, k = rows, the heads, head_dim and dtype; it carries nothing from
- * call to call. bf16 (products of bf16 values on the tensor cores, sums and
- * softmax in fp32) or fp32 (CUDA cores).
+ * call to call. fp32 (CUDA cores) or bf16: products of bf16 values on the tensor
+ * cores, logits, maxima, sums and lse in fp32, the softmax's weights rounded to
+ * bf16 for the product with the values (2^-8 of each; their sum is that of the
+ * weights before). bf16 calls of up to 16 (token, query head of a KV head's
+ * group) pairs a request on average, empty requests counted, go to a kernel
+ * that reads the keys once for every 16 such rows, others to one of 256 rows;
+ * a call that mixes both kinds is right either way, and faster as two.
  */
 tg_status tg_paged_attn(const tg_paged_kv* cache, const void* q, int64_t q_stride, int64_t rows,
                         const int32_t* cu_q, const int32_t* kv_len, int32_t batch, int32_t hq,

@@ -785,7 +785,8 @@ def tg_paged_append(cache: PagedKV, k, v, cu_q, kv_len, q=None, pos=None, s=None
     """Appends the new rows of a batch of requests to the cache: per-head
     RMSNorm of q and k (where a weight is given), rotation at pos (None: the
     row's index in its request; rope_base 0: none), k, v and the gate biases
-    logsigmoid(s) into the pages. k, v [rows, hkv, dh], q [rows, hq, dh] or
+    logsigmoid(s) into the pages (None: 0, the bias of generated rows; beside
+    kept ones these have s = +inf). k, v [rows, hkv, dh], q [rows, hq, dh] or
     None, all possibly slices of one fused projection; cu_q [batch + 1],
     kv_len [batch] (the new rows included) int32. Returns the rotated queries
     [rows, hq, dh], or None without q."""

@@ -16,6 +16,11 @@
 // CTA writes the output; otherwise it writes its unnormalised rows and their
 // (maximum, sum), and paged_merge adds up the splits in their order.
 //
+// Weights P are rounded to bf16 (2^-8 of each), as the tensor core multiplies
+// them with bf16 values at full rate; P in two bf16 parts would double the
+// second product. Logits, maxima, sums (of the weights before that rounding)
+// and outputs up to the last rounding are fp32.
+//
 // Why mma.sync: 16 rows use an eighth of a tcgen05 tile (M = 128), whose
 // softmax would run one thread per row; here all 128 threads hold logits, and
 // the tensor work is a fifth of the time that the keys take to arrive.

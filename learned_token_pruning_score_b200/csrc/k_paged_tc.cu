@@ -22,6 +22,11 @@
 // per warpgroup means that S(j + 1) is seen only after PV(j) has finished, so O
 // may be rescaled and P overwritten without another wait.
 //
+// P is rounded to bf16 (2^-8 of each weight), the type of the values that the
+// tensor core multiplies it with: an fp32 or two-part P would take the 128 TMEM
+// columns of S and as much of the tensor core again. Logits, maxima, sums (of
+// the weights before that rounding) and O up to the last rounding are fp32.
+//
 // Gate bias: one more 16-wide K-step adds g b with g = gain sqrt(dh) tau, each
 // of g and b in three bf16 parts and the six products down to 2^-24 kept. Keys
 // whose bias is below -1e20 get b = 0 there and are decided one by one in fp32.

@@ -406,7 +406,8 @@ inline int64_t paged_row_tiles(int64_t rows, int64_t batch, int hq, int hkv, int
 }
 // bf16: rows of a tile. Up to 16 rows of a request and KV head on average the
 // keys are what the call is made of (16, k_paged_decode.cu); above, the tensor
-// cores' tiles (256, k_paged_tc.cu).
+// cores' tiles (256, k_paged_tc.cu). The lengths of single requests are device
+// data: one long chunk among many single tokens goes the way of the mean.
 inline int paged_tile_rows(int64_t rows, int64_t batch, int hq, int hkv) {
   return rows * (hq / hkv) <= 16 * batch ? 16 : 256;
 }
