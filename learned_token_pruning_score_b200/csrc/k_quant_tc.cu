@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (++s == p.stages) { s = 0; ph ^= 1u; }
     }
     if (ok) umma_commit(acc_full);
-    else s_bad = 1;  // the sums are not complete: nothing is stored
+    else s_bad = 1;  // the sums are not complete: this part's columns are not stored
   }
   // The ring is free once the last MMA has read it: the sums go there.
   int* sums = reinterpret_cast<int*>(tiles);
